@@ -260,6 +260,102 @@ rcp_status rcp_prefill_reconstruct_workspace_size(const rcp_cache* cache, int32_
  * ceil(R d / (R - d)) (147 for R = 1024, d = 128); INT32_MAX when R <= d. */
 rcp_status rcp_prefill_crossover_rows(const rcp_cache* cache, int32_t* rows);
 
+/* Score modifications of an attention call, for models whose scores are not plain products.
+ * Row r of the call's queries, of request b, sits at position pos (decode: seq_lens[b] - 1;
+ * chunk row i: seq_lens[b] - chunk_b + i) and attends the tokens t that it sees:
+ *     t < seq_lens[b]  and  (t < prefix_lens[b]  or
+ *                            (row_begin[r] <= t <= pos  and  t > pos - window))
+ * with scores
+ *     s = q~_h . c_k[t,h] / sqrt(d);   s = softcap tanh(s / softcap);
+ *     s = s - alibi_slopes[h] |pos - t|.
+ * A row that sees no token gives zeros.  A zero or NULL member leaves its part out:
+ *   softcap       cap of the scores, 0 or in [2^-10, 2^20];
+ *   alibi_slopes  [H] fp32 device, finite: a bias that falls with the distance;
+ *   window        >= 0: the last `window` tokens up to and including the row's own;
+ *   prefix_lens   [batch] int32 device: tokens that every row of the request sees, whatever
+ *                 its position (a prefix mask, where rows of the prefix also see later ones of
+ *                 it; with a window, the tokens that stay visible behind it).  Negative
+ *                 counts as 0, more than seq_lens[b] as seq_lens[b];
+ *   row_begin     [query rows] int32 device: the first token the row sees behind the prefix (a
+ *                 document mask: the start of the row's document).  Negative counts as 0.
+ * Distances and positions count cached tokens.  Tokens that no row of a request sees take no
+ * part whatever their slots hold, and pages before every row's first token and behind the
+ * prefix are not read (their blocks may have been freed, their table entries are not looked
+ * at).  A row's result does depend on non-finite coefficients of tokens that other rows of
+ * its chunk see. */
+typedef struct rcp_score_mod {
+  float softcap;
+  int32_t window;
+  const float* alibi_slopes;
+  const int32_t* prefix_lens;
+  const int32_t* row_begin;
+} rcp_score_mod;
+
+/* rcp_decode_step and rcp_prefill_step with score modifications: the same arguments, results,
+ * workspaces and errors otherwise.  With num_tokens = 0 nothing is appended (k, v and
+ * slot_mapping are not read): the attention alone.  mod may be NULL (the plain call); a
+ * softcap outside its range, a negative window, a misaligned member or max_blocks_per_seq
+ * above 2^26 is RCP_ERR_INVALID_ARG.  mod itself is host memory, read during the call. */
+rcp_status rcp_decode_step_mod(rcp_cache* cache, const void* k, const void* v,
+                               const int64_t* slot_mapping, int32_t num_tokens, const void* q,
+                               const int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t batch, const rcp_score_mod* mod,
+                               void* out, void* workspace, size_t workspace_bytes,
+                               rcp_stream stream);
+rcp_status rcp_prefill_step_mod(rcp_cache* cache, const void* k, const void* v,
+                                const int64_t* slot_mapping, int32_t num_tokens, const void* q,
+                                const int32_t* cu_chunk_lens, int32_t num_query_rows,
+                                const int32_t* block_table, int32_t max_blocks_per_seq,
+                                const int32_t* seq_lens, int32_t batch, int32_t reconstruct,
+                                const rcp_score_mod* mod, void* out, void* workspace,
+                                size_t workspace_bytes, rcp_stream stream);
+
+/* Copies pages (copy-on-write of a shared page): pair i copies the K and V page of block
+ * pairs[2 i] to block pairs[2 i + 1], every byte.  pairs: [num_pairs][2] int32 device.  A
+ * pair with -1 in it is skipped; another id outside [0, num_blocks) sets RCP_DEVERR_BAD_BLOCK
+ * and its pair copies nothing.  A destination that occurs twice, or that is another pair's
+ * source, gets undefined contents.  Host pool and references are not touched. */
+rcp_status rcp_copy_blocks(rcp_cache* cache, const int32_t* pairs, int32_t num_pairs,
+                           rcp_stream stream);
+
+/* References to blocks of the pool, for sequences that share pages.  rcp_alloc_blocks hands
+ * out blocks with one reference; fork adds one to each listed block (host array; a block
+ * listed twice gets two) and rcp_free_blocks takes one away and returns the block to the
+ * pool with its last.  RCP_ERR_CAPACITY and no change on an out-of-range or free id or a
+ * reference count past 2^31 - 1.  block_refs writes each listed block's count (0: free). */
+rcp_status rcp_fork_blocks(rcp_cache* cache, int32_t n, const int32_t* ids);
+rcp_status rcp_block_refs(const rcp_cache* cache, int32_t n, const int32_t* ids,
+                          int32_t* refs_out);
+
+/* Forks a sequence of `length` tokens in the blocks ids[0 .. num_blocks) (host array) into
+ * num_children more.  Each child shares the parent's full pages (one more reference each)
+ * and gets a block of its own for the last, partly filled one, copied on the stream.
+ * child_ids: host [num_children][ceil(length / 16)], each child's blocks in order (blocks of
+ * the parent past those are not shared).  RCP_ERR_CAPACITY and no change if a block is not in
+ * use or fewer blocks are free than children need; RCP_ERR_INVALID_ARG if num_blocks is less
+ * than ceil(length / 16).  The block ids are part of the queued copy: a captured graph
+ * replays it with the same ones. */
+rcp_status rcp_fork_sequence(rcp_cache* cache, const int32_t* ids, int32_t num_blocks,
+                             int32_t length, int32_t num_children, int32_t* child_ids,
+                             rcp_stream stream);
+
+/* Drops tokens of every request in place: token t < seq_lens[b] stays if keep[b][t] != 0, and
+ * the kept ones move, in order, to the first positions of the request's pages;
+ * new_lens[b] = their number.  Slots from new_lens[b] on keep what they held, and so does a
+ * page whose tokens all stay where they are (it may be shared with other requests; a page
+ * that a token moves to may not).  keep: [batch][max_blocks_per_seq * 16] uint8 device
+ * (16-byte aligned); block_table, seq_lens as for decode; new_lens: [batch] int32 device, not
+ * overlapping seq_lens.  The caller frees the pages past ceil(new_lens[b] / 16) once it has
+ * read new_lens.  Device errors: a length outside the table sets RCP_DEVERR_BAD_LEN, its
+ * request stays as it is and new_lens[b] = 0; a bad block id on a move's way sets
+ * RCP_DEVERR_BAD_BLOCK and that token is not moved.  RCP_ERR_INVALID_ARG for null,
+ * misaligned or overlapping arguments or max_blocks_per_seq above 2^26,
+ * RCP_ERR_UNSUPPORTED for a batch above 2^20. */
+rcp_status rcp_compact_tokens(rcp_cache* cache, const int32_t* block_table,
+                              int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                              const uint8_t* keep, int32_t batch, int32_t* new_lens,
+                              rcp_stream stream);
+
 /* Measurement hook (the pages have no counterpart; it exists for roofline timing).  When
  * both events are non-NULL, every later decode / prefill call records start_event on its
  * stream just before the split-K attention kernel and stop_event just after it, so the

@@ -484,3 +484,142 @@ def prefill_attn(q, cu_chunk_lens, k_pages, v_pages, U_k, W_v, block_table, seq_
         o, _ = attend(q[c0:c1], ck, cv, U_k, W_v, d, n_keys=n_keys)
         out[c0:c1] = o
     return out
+
+
+# ------------------------------------------------------------------ score modifications
+# Capped scores, distance bias and masks beyond the causal one (the pages have no counterpart:
+# they serve models that need them).  A row at position pos of a request with L tokens sees
+# t < L with t < prefix, or begin <= t <= pos and t > pos - window (window 0: no limit), with
+# scores s = cap tanh(s / cap) (cap 0: as they are), then s - slope_h |pos - t|.
+
+def visible_tokens(pos: int, L: int, prefix: int = 0, begin: int = 0, window: int = 0):
+    """Bool [L]: the tokens a row sees, one by one as defined."""
+    out = np.zeros(int(L), bool)
+    for t in range(int(L)):
+        behind = begin <= t <= pos and (window == 0 or t > pos - window)
+        out[t] = t < prefix or behind
+    return out
+
+
+def attend_mod(q, ck, cv, U_k, W_v, head_dim: int, positions, see, softcap: float = 0.0,
+               slopes=None):
+    """Modified attention of the rows q [n][H][d] at ``positions`` over one request's
+    coefficients; see: bool [n][L].  Returns (o [n][H][d], p [n][H][L]) in fp64.  Tokens that
+    no row sees take no part, whatever their coefficients."""
+    q, U, W = _f64(q), _f64(U_k), _f64(W_v)
+    see = np.asarray(see, bool)
+    n, H, d = q.shape
+    L = ck.shape[0]
+    o, p = np.zeros((n, H, d)), np.zeros((n, H, L))
+    idx = np.nonzero(see.any(axis=0))[0]
+    if idx.size == 0:
+        return o, p
+    pos = np.asarray(positions, np.float64)
+    for h in range(H):
+        s = (q[:, h] @ U[h].T) @ ck[idx, h].T / np.sqrt(head_dim)        # [n][idx]
+        if softcap > 0:
+            s = softcap * np.tanh(s / softcap)
+        if slopes is not None:
+            s = s - float(slopes[h]) * np.abs(pos[:, None] - idx[None, :])
+        v = see[:, idx]
+        for i in range(n):
+            w = np.nonzero(v[i])[0]
+            if w.size == 0:
+                continue
+            e = np.exp(s[i, w] - s[i, w].max())
+            p[i, h, idx[w]] = e / e.sum()
+        o[:, h] = (p[:, h][:, idx] @ cv[idx]) @ W[:, h * d:(h + 1) * d]
+    return o, p
+
+
+def prefill_attn_mod(q, cu_chunk_lens, k_pages, v_pages, U_k, W_v, block_table, seq_lens,
+                     block_size: int = 16, softcap: float = 0.0, alibi_slopes=None,
+                     window: int = 0, prefix_lens=None, row_begin=None, magnitudes: bool = False):
+    """Modified chunked-prefill attention (a decode is a chunk of one row per request).  Returns
+    o [rows][H][d]; with ``magnitudes`` also sum_t p |V^_t| per output element and, per row,
+    the largest sum_k |q~_k c_k| / sqrt(d) of a visible score, the numbers that rounding error
+    bounds are made of."""
+    q = np.asarray(q)
+    T, H, d = q.shape
+    out, mag, prod = np.zeros((T, H, d)), np.zeros((T, H, d)), np.zeros(T)
+    for b in range(len(seq_lens)):
+        c0, c1 = int(cu_chunk_lens[b]), int(cu_chunk_lens[b + 1])
+        n, L = c1 - c0, int(seq_lens[b])
+        if n == 0 or L == 0:
+            continue
+        pos = L - n + np.arange(n)
+        pre = 0 if prefix_lens is None else int(prefix_lens[b])
+        see = np.stack([visible_tokens(int(pos[i]), L, pre,
+                                       0 if row_begin is None else int(row_begin[c0 + i]), window)
+                        for i in range(n)])
+        used = np.nonzero(see.any(axis=0))[0]
+        table = np.array(block_table[b])
+        hidden = np.ones(len(table), bool)
+        hidden[used // block_size] = False
+        table[hidden] = 0                                  # entries that are not looked at
+        ck, cv = gather_request(k_pages, v_pages, table, L, block_size)
+        o, p = attend_mod(q[c0:c1], ck, cv, U_k, W_v, d, pos, see, softcap, alibi_slopes)
+        out[c0:c1] = o
+        if magnitudes and used.size:
+            for h in range(H):
+                vh = np.abs(cv[used] @ _f64(W_v)[:, h * d:(h + 1) * d])
+                mag[c0:c1, h] = p[:, h][:, used] @ vh
+                qt = _f64(q[c0:c1, h]) @ _f64(U_k)[h].T
+                s = np.abs(qt) @ np.abs(ck[used, h]).T / np.sqrt(d)
+                prod[c0:c1] = np.maximum(prod[c0:c1], np.where(see[:, used], s, 0).max(axis=1))
+    return (out, mag, prod) if magnitudes else out
+
+
+def decode_attn_mod(q, k_pages, v_pages, U_k, W_v, block_table, seq_lens, block_size: int = 16,
+                    **mod):
+    """Modified decode attention: one row per request, at the request's last position."""
+    cu = np.arange(len(seq_lens) + 1)
+    return prefill_attn_mod(q, cu, k_pages, v_pages, U_k, W_v, block_table, seq_lens, block_size,
+                            **mod)
+
+
+def compact_moves(block_table_row, seq_len: int, keep_row, block_size: int = 16):
+    """(source slots, destination slots) of one request's kept tokens, in order."""
+    src = [t for t in range(int(seq_len)) if keep_row[t]]
+    row = np.asarray(block_table_row, np.int64)
+
+    def slot(t):
+        t = np.asarray(t, np.int64)
+        return row[t // block_size] * block_size + t % block_size
+    return slot(src), slot(np.arange(len(src)))
+
+
+def token_rows(k_pages, v_pages, page_format: str, num_heads: int, rank_k: int, rank_v: int,
+               block_size: int = 16):
+    """The bytes of every slot's token: a list of uint8 views [num_blocks][rows][16][width] of
+    the pages, whatever the format (writing to them writes the pages)."""
+    H, bs = num_heads, block_size
+    if page_format == "int4":
+        kc, vc = H * bs * rank_k // 2, bs * rank_v // 2
+        nb = k_pages.shape[0]
+        return [k_pages[:, :kc].reshape(nb, H, bs, -1), k_pages[:, kc:].reshape(nb, H, bs, 2),
+                v_pages[:, :vc].reshape(nb, 1, bs, -1), v_pages[:, vc:].reshape(nb, 1, bs, -1)]
+    k, v = k_pages.view(np.uint8), v_pages.view(np.uint8)
+    return [k.reshape(*k_pages.shape[:3], -1), v.reshape(v_pages.shape[0], 1, bs, -1)]
+
+
+def compact_tokens(k_pages, v_pages, page_format: str, shape: dict, block_table, seq_lens, keep,
+                   block_size: int = 16):
+    """Pages after dropping tokens, and the new lengths: copies (k, v, lens)."""
+    k, v = k_pages.copy(), v_pages.copy()
+    dims = (page_format, shape["num_heads"], shape["rank_k"], shape["rank_v"], block_size)
+    if page_format == "int4":
+        kc = shape["num_heads"] * block_size * shape["rank_k"] // 2
+        vc = block_size * shape["rank_v"] // 2
+    lens = []
+    for b, L in enumerate(seq_lens):
+        src, dst = compact_moves(block_table[b], L, keep[b], block_size)
+        lens.append(len(src))
+        old = token_rows(k_pages, v_pages, *dims)
+        new = token_rows(k, v, *dims)
+        for o, n in zip(old, new):
+            n[dst // block_size, :, dst % block_size] = o[src // block_size, :, src % block_size]
+        if page_format == "int4":   # reshapes of column slices are copies: put them back
+            k[:, :kc], k[:, kc:] = new[0].reshape(k.shape[0], -1), new[1].reshape(k.shape[0], -1)
+            v[:, :vc], v[:, vc:] = new[2].reshape(v.shape[0], -1), new[3].reshape(v.shape[0], -1)
+    return k, v, np.array(lens, np.int32)

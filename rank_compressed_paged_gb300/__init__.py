@@ -9,6 +9,9 @@ step of the path runs in the library's CUDA kernels.
     cache.append_kv(k, v, slot_mapping)                          # project + scatter
     out = cache.decode_attn(q, block_table, seq_lens)            # [B][H][d] fp16
     out = cache.prefill_attn(q, cu_chunk_lens, block_table, seq_lens)
+    out = cache.decode_attn(q, block_table, seq_lens, mod=ScoreMod(softcap=30.0, window=4096))
+    child, = cache.fork_sequence(ids, length)                    # shares pages, copies the last
+    new_lens = cache.compact_tokens(block_table, seq_lens, keep) # drops tokens in place
 """
 from __future__ import annotations
 
@@ -93,6 +96,46 @@ def _validate_workspace(device, ws) -> None:
     _need("workspace", ws, torch.uint8, (None,), device)
 
 
+def _validate_mod(device, H: int, B: int, rows: int, mod) -> None:
+    """The tensors of a ScoreMod for B requests with ``rows`` query rows."""
+    import torch
+    if not isinstance(mod, ScoreMod):
+        raise ValueError(f"mod must be a ScoreMod, got {type(mod).__name__}")
+    if mod.alibi_slopes is not None:
+        _need("alibi_slopes", mod.alibi_slopes, torch.float32, (H,), device)
+    if mod.prefix_lens is not None:
+        _need("prefix_lens", mod.prefix_lens, torch.int32, (B,), device)
+    if mod.row_begin is not None:
+        _need("row_begin", mod.row_begin, torch.int32, (rows,), device)
+
+
+def _validate_compact(device, block_table, seq_lens, keep, new_lens) -> int:
+    """block_table: [>= B][max_blocks] int32; seq_lens, new_lens: [B] int32; keep:
+    [B][max_blocks * 16] uint8.  Returns B."""
+    import torch
+    _need("seq_lens", seq_lens, torch.int32, (None,), device)
+    B = int(seq_lens.shape[0])
+    _need("block_table", block_table, torch.int32, (None, None), device)
+    if block_table.shape[0] < B or block_table.shape[1] < 1:
+        raise ValueError(f"block_table needs at least {B} rows and one column, "
+                         f"got {list(block_table.shape)}")
+    _need("keep", keep, torch.uint8, (B, int(block_table.shape[1]) * BLOCK_SIZE), device)
+    _need("new_lens", new_lens, torch.int32, (B,), device)
+    return B
+
+
+def _on_current(device) -> None:
+    """The library launches on the current device, which has to be the cache's."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the cache is on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _ids(ids):
+    return (ctypes.c_int32 * max(len(ids), 1))(*ids)
+
+
 def _stream(stream=None) -> int:
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
@@ -105,6 +148,37 @@ def int4_page_bytes(num_heads: int, rank_k: int, rank_v: int):
     k = num_heads * BLOCK_SIZE * rank_k // 2 + num_heads * BLOCK_SIZE * 2
     v = BLOCK_SIZE * rank_v // 2 + BLOCK_SIZE * (rank_v // 64) * 2
     return k, v
+
+
+class ScoreMod:
+    """Score modifications of an attention call (include/rcp.h, rcp_score_mod): the row at
+    position pos sees tokens t < prefix_lens[b], and tokens row_begin[row] <= t <= pos with
+    t > pos - window, with scores softcap * tanh(s / softcap) - alibi_slopes[h] * |pos - t|.
+    What is left at 0 / None takes no part.
+
+    softcap: 0, or between 2**-10 and 2**20; window: tokens, the row's own included;
+    alibi_slopes: [H] float32; prefix_lens: [B] int32; row_begin: [query rows] int32 (decode: [B],
+    a document mask's start of the row's document).  The tensors are read by the kernels, on
+    the call's stream.
+    """
+
+    __slots__ = ("softcap", "alibi_slopes", "window", "prefix_lens", "row_begin")
+
+    def __init__(self, softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                 prefix_lens=None, row_begin=None):
+        self.softcap = float(softcap)
+        self.alibi_slopes = alibi_slopes
+        self.window = int(window)
+        self.prefix_lens = prefix_lens
+        self.row_begin = row_begin
+        if not -2**31 <= self.window < 2**31:
+            raise ValueError(f"window must fit 32 bits, got {self.window}")
+
+    def _args(self):
+        def at(x):
+            return None if x is None else _ptr(x)
+        return _lib.ScoreModArgs(self.softcap, self.window, at(self.alibi_slopes),
+                                 at(self.prefix_lens), at(self.row_begin))
 
 
 class PagedCoeffCache:
@@ -190,6 +264,53 @@ class PagedCoeffCache:
         _lib.check("rcp_num_free_blocks", self._lib.rcp_num_free_blocks(self._h, ctypes.byref(n)))
         return n.value
 
+    def fork_blocks(self, ids) -> None:
+        """One more reference to each block (free_blocks takes one away, and returns a block to
+        the pool with its last)."""
+        _lib.check("rcp_fork_blocks", self._lib.rcp_fork_blocks(self._h, len(ids), _ids(ids)))
+
+    def block_refs(self, ids):
+        """References to each block (0: free)."""
+        refs = (ctypes.c_int32 * max(len(ids), 1))()
+        _lib.check("rcp_block_refs",
+                   self._lib.rcp_block_refs(self._h, len(ids), _ids(ids), refs))
+        return [refs[i] for i in range(len(ids))]
+
+    def fork_sequence(self, ids, length: int, children: int = 1, stream=None):
+        """Forks the sequence of ``length`` tokens in blocks ``ids``: returns ``children`` lists
+        of block ids, each sharing the full pages and holding a copy of the last, partly
+        filled one (queued on the stream)."""
+        _on_current(self.device)
+        n = -(-int(length) // BLOCK_SIZE)
+        out = (ctypes.c_int32 * max(n * int(children), 1))()
+        _lib.check("rcp_fork_sequence", self._lib.rcp_fork_sequence(
+            self._h, _ids(ids), len(ids), int(length), int(children), out, _stream(stream)))
+        return [[out[c * n + j] for j in range(n)] for c in range(int(children))]
+
+    def copy_blocks(self, pairs, stream=None) -> None:
+        """Copies K and V pages: pairs [n][2] int32 on the cache's device, (source, destination)
+        block ids; a pair with -1 in it is skipped."""
+        import torch
+        _need("pairs", pairs, torch.int32, (None, 2), self.device)
+        _on_current(self.device)
+        _lib.check("rcp_copy_blocks", self._lib.rcp_copy_blocks(
+            self._h, _ptr(pairs), int(pairs.shape[0]), _stream(stream)))
+
+    def compact_tokens(self, block_table, seq_lens, keep, new_lens=None, stream=None):
+        """Drops tokens in place: token t of request b stays if keep[b][t] != 0, the kept ones
+        move to the front of the request's pages.  keep: [B][max_blocks * 16] uint8.  Returns
+        the new lengths [B] int32 (``new_lens``, which must not be ``seq_lens``); the pages past
+        them may then be freed."""
+        import torch
+        if new_lens is None:
+            new_lens = torch.empty_like(seq_lens)
+        B = _validate_compact(self.device, block_table, seq_lens, keep, new_lens)
+        _on_current(self.device)
+        _lib.check("rcp_compact_tokens", self._lib.rcp_compact_tokens(
+            self._h, _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), _ptr(keep), B,
+            _ptr(new_lens), _stream(stream)))
+        return new_lens
+
     # ------------------------------------------------------------------ workspace
     def workspace_bytes(self, rows: int) -> int:
         n = ctypes.c_size_t()
@@ -242,8 +363,22 @@ class PagedCoeffCache:
         _lib.check("rcp_append_kv", self._lib.rcp_append_kv(
             self._h, _ptr(k), _ptr(v), _ptr(slot_mapping), T, _stream(stream)))
 
-    def decode_attn(self, q, block_table, seq_lens, out=None, workspace=None, stream=None):
-        """q: [B][H][d] fp16; block_table: [B][max_blocks] int32; seq_lens: [B] int32."""
+    def _decode_mod(self, mod, app, q, block_table, seq_lens, out, ws, stream):
+        """rcp_decode_step_mod; app: (k, v, slot_mapping), or None for the attention alone."""
+        H, B = self.shape["num_heads"], int(seq_lens.shape[0])
+        _validate_mod(self.device, H, B, B, mod)
+        _on_current(self.device)
+        k, v, slots, T = (None, None, None, 0) if app is None else (
+            _ptr(app[0]), _ptr(app[1]), _ptr(app[2]), int(app[2].shape[0]))
+        _lib.check("rcp_decode_step_mod", self._lib.rcp_decode_step_mod(
+            self._h, k, v, slots, T, _ptr(q), _ptr(block_table), int(block_table.shape[1]),
+            _ptr(seq_lens), B, ctypes.byref(mod._args()), _ptr(out), _ptr(ws),
+            ws.numel() * ws.element_size(), _stream(stream)))
+
+    def decode_attn(self, q, block_table, seq_lens, out=None, workspace=None, stream=None,
+                    mod=None):
+        """q: [B][H][d] fp16; block_table: [B][max_blocks] int32; seq_lens: [B] int32; mod: None
+        or a ScoreMod."""
         import torch
         if out is None:
             out = torch.empty_like(q)
@@ -251,6 +386,9 @@ class PagedCoeffCache:
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
         ws = self.workspace(B) if workspace is None else workspace
         _validate_workspace(self.device, ws)
+        if mod is not None:
+            self._decode_mod(mod, None, q, block_table, seq_lens, out, ws, stream)
+            return out
         _lib.check("rcp_decode_attn", self._lib.rcp_decode_attn(
             self._h, _ptr(q), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), B,
             _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
@@ -278,8 +416,8 @@ class PagedCoeffCache:
         return out
 
     def decode_step(self, k, v, slot_mapping, q, block_table, seq_lens, out=None, workspace=None,
-                    stream=None):
-        """append_kv(k, v, slot_mapping) then decode_attn(q, ...), queued as one step."""
+                    stream=None, mod=None):
+        """append_kv(k, v, slot_mapping) then decode_attn(q, ..., mod=mod), queued as one step."""
         import torch
         if out is None:
             out = torch.empty_like(q)
@@ -288,6 +426,9 @@ class PagedCoeffCache:
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
         ws = self.workspace(B) if workspace is None else workspace
         _validate_workspace(self.device, ws)
+        if mod is not None:
+            self._decode_mod(mod, (k, v, slot_mapping), q, block_table, seq_lens, out, ws, stream)
+            return out
         _lib.check("rcp_decode_step", self._lib.rcp_decode_step(
             self._h, _ptr(k), _ptr(v), _ptr(slot_mapping), int(slot_mapping.shape[0]), _ptr(q),
             _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), B, _ptr(out), _ptr(ws),
@@ -308,9 +449,24 @@ class PagedCoeffCache:
             return self.workspace(rows, self.workspace_bytes(rows))
         return self.workspace(rows, self.reconstruct_workspace_bytes(rows, B, mb))
 
+    def _prefill_mod(self, mod, app, q, cu_chunk_lens, block_table, seq_lens, out, ws, stream,
+                     variant: str):
+        """rcp_prefill_step_mod; app: (k, v, slot_mapping), or None for the attention alone."""
+        H, B, rows = self.shape["num_heads"], int(seq_lens.shape[0]), int(q.shape[0])
+        _validate_mod(self.device, H, B, rows, mod)
+        _on_current(self.device)
+        k, v, slots, T = (None, None, None, 0) if app is None else (
+            _ptr(app[0]), _ptr(app[1]), _ptr(app[2]), int(app[2].shape[0]))
+        _lib.check("rcp_prefill_step_mod", self._lib.rcp_prefill_step_mod(
+            self._h, k, v, slots, T, _ptr(q), _ptr(cu_chunk_lens), rows, _ptr(block_table),
+            int(block_table.shape[1]), _ptr(seq_lens), B, 1 if variant == "reconstruct" else 0,
+            ctypes.byref(mod._args()), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
+            _stream(stream)))
+
     def prefill_attn(self, q, cu_chunk_lens, block_table, seq_lens, out=None, workspace=None,
-                     stream=None, variant: str = "auto"):
-        """q: [sum chunk][H][d] fp16; cu_chunk_lens: [B+1] int32; seq_lens include the chunk.
+                     stream=None, variant: str = "auto", mod=None):
+        """q: [sum chunk][H][d] fp16; cu_chunk_lens: [B+1] int32; seq_lens include the chunk;
+        mod: None or a ScoreMod.
 
         variant: "rank" (joint-coefficient contraction per head), "reconstruct" (dense values
         C_v W_v rebuilt once per key), or "auto": reconstruct when chunks average at least
@@ -327,6 +483,11 @@ class PagedCoeffCache:
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B)
         ws = self._prefill_workspace(variant, rows, B, mb) if workspace is None else workspace
+        if mod is not None:
+            _validate_workspace(self.device, ws)
+            self._prefill_mod(mod, None, q, cu_chunk_lens, block_table, seq_lens, out, ws, stream,
+                              variant)
+            return out
         if variant == "rank":
             fn, name = self._lib.rcp_prefill_attn, "rcp_prefill_attn"
         else:
@@ -338,9 +499,9 @@ class PagedCoeffCache:
         return out
 
     def prefill_step(self, k, v, slot_mapping, q, cu_chunk_lens, block_table, seq_lens,
-                     out=None, workspace=None, stream=None, variant: str = "auto"):
-        """append_kv(k, v, slot_mapping) then prefill_attn(q, cu_chunk_lens, ...), queued as
-        one step (the chunk's query projection shares the append's launch).  Arguments and
+                     out=None, workspace=None, stream=None, variant: str = "auto", mod=None):
+        """append_kv(k, v, slot_mapping) then prefill_attn(q, cu_chunk_lens, ..., mod=mod), queued
+        as one step (the chunk's query projection shares the append's launch).  Arguments and
         variant choice as the two calls."""
         import torch
         if out is None:
@@ -353,6 +514,10 @@ class PagedCoeffCache:
         variant = self._prefill_variant(variant, rows, B)
         ws = self._prefill_workspace(variant, rows, B, mb) if workspace is None else workspace
         _validate_workspace(self.device, ws)
+        if mod is not None:
+            self._prefill_mod(mod, (k, v, slot_mapping), q, cu_chunk_lens, block_table, seq_lens,
+                              out, ws, stream, variant)
+            return out
         _lib.check("rcp_prefill_step", self._lib.rcp_prefill_step(
             self._h, _ptr(k), _ptr(v), _ptr(slot_mapping), T, _ptr(q), _ptr(cu_chunk_lens), rows,
             _ptr(block_table), mb, _ptr(seq_lens), B, 1 if variant == "reconstruct" else 0,

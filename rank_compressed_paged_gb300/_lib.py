@@ -29,6 +29,12 @@ class CacheConfig(ctypes.Structure):
                 ("page_format", ctypes.c_int32)]
 
 
+class ScoreModArgs(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("row_begin", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -54,6 +60,19 @@ _SIG = {
                                                     _P, ctypes.c_size_t, _P]),
     "rcp_prefill_step": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P, _I32,
                                         _I32, _P, _P, ctypes.c_size_t, _P]),
+    "rcp_decode_step_mod": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _P, _I32,
+                                           ctypes.POINTER(ScoreModArgs), _P, _P, ctypes.c_size_t,
+                                           _P]),
+    "rcp_prefill_step_mod": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _P, _I32, _P,
+                                            _I32, _I32, ctypes.POINTER(ScoreModArgs), _P, _P,
+                                            ctypes.c_size_t, _P]),
+    "rcp_copy_blocks": (ctypes.c_int, [_P, _P, _I32, _P]),
+    "rcp_fork_blocks": (ctypes.c_int, [_P, _I32, ctypes.POINTER(ctypes.c_int32)]),
+    "rcp_block_refs": (ctypes.c_int, [_P, _I32, ctypes.POINTER(ctypes.c_int32),
+                                      ctypes.POINTER(ctypes.c_int32)]),
+    "rcp_fork_sequence": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _I32, _I32, _I32,
+                                         ctypes.POINTER(ctypes.c_int32), _P]),
+    "rcp_compact_tokens": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I32, _P, _P]),
     "rcp_prefill_reconstruct_workspace_size": (ctypes.c_int, [_P, _I32, _I32, _I32,
                                                               ctypes.POINTER(ctypes.c_size_t)]),
     "rcp_prefill_crossover_rows": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32)]),

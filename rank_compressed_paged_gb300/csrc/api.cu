@@ -29,6 +29,7 @@ struct rcp_cache {
   int shape;
   std::vector<int32_t> free_ids;   // LIFO stack of free physical blocks
   std::vector<uint8_t> is_free;
+  std::vector<int32_t> refs;       // references to each block in use (0: free)
   // device-side state, set up at the first kernel call on a device
   int device;
   int num_sms;
@@ -210,6 +211,7 @@ void fill_ws(rcp::AttnParams& p, void* ws, int64_t nq) {
   p.qlo = b + w.qt + static_cast<size_t>(nq) * S::H * 64 * 2;
   p.vcum = nullptr;
   p.vhat = nullptr;
+  p.vmap = nullptr;
 }
 
 // E4M3 pages: fp16 copies of the batch's pages for the reconstructing prefill
@@ -225,6 +227,7 @@ Widened fill_recon(rcp::AttnParams& p, void* ws, int64_t nq, int64_t batch, int6
   const rcp::ReconLayout r = rcp::recon_layout<S>(nq, batch, max_blocks, widen);
   uint8_t* b = static_cast<uint8_t*>(ws);
   p.vcum = reinterpret_cast<int64_t*>(b + r.vcum);
+  if (p.mod) p.vmap = reinterpret_cast<int32_t*>(b + r.vmap);
   p.vhat = b + r.vhat;
   if (!widen) return Widened{nullptr, nullptr, nullptr};
   return Widened{b + r.kw, b + r.vw, reinterpret_cast<int32_t*>(b + r.tw)};
@@ -307,13 +310,58 @@ rcp_status launch_front(rcp_cache* c, const AppendArgs* app, const void* q, int3
   return e == cudaSuccess ? RCP_OK : RCP_ERR_CUDA;
 }
 
+constexpr int32_t kMaxTableWidth = 1 << 26;     // token positions stay below 2^30
+constexpr int32_t kMaxCompactBatch = 1 << 20;   // CTAs of one launch stay below 2^31
+
+// RCP_OK if every listed block is in use and can take `more` further references in all.
+rcp_status check_forkable(const rcp_cache* c, int32_t n, const int32_t* ids, int64_t more) {
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t id = ids[i];
+    if (id < 0 || id >= c->cfg.num_blocks || c->is_free[static_cast<size_t>(id)])
+      return RCP_ERR_CAPACITY;
+    if (c->refs[static_cast<size_t>(id)] > INT32_MAX - more) return RCP_ERR_CAPACITY;
+  }
+  return RCP_OK;
+}
+
+cudaError_t copy_pages(rcp_cache* c, const rcp::CopyParams& p, const int32_t* list,
+                       rcp_stream stream) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return c->shape == kShapeMain
+             ? rcp::launch_copy_pages<ShapeMain>(p, list, c->cfg.page_format, c->num_sms, s)
+             : rcp::launch_copy_pages<ShapeTiny>(p, list, c->cfg.page_format, c->num_sms, s);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Largest and least score caps: between them s / cap and its square stay far from fp32's
+// limits for every score that fp16 inputs give.
+constexpr float kMinSoftcap = 1.f / 1024, kMaxSoftcap = 1048576.f;
+
+rcp_status check_mod(const rcp_score_mod& m) {
+  if (!(m.softcap == 0.f || (m.softcap >= kMinSoftcap && m.softcap <= kMaxSoftcap)))   // NaN too
+    return RCP_ERR_INVALID_ARG;
+  if (m.window < 0) return RCP_ERR_INVALID_ARG;
+  if (!aligned4(m.alibi_slopes) || !aligned4(m.prefix_lens) || !aligned4(m.row_begin))
+    return RCP_ERR_INVALID_ARG;
+  return RCP_OK;
+}
+
+// Whether a call's modifications change anything (a call that sets none is the plain one).
+bool modifies(const rcp_score_mod* m) {
+  return m && (m->softcap > 0.f || m->alibi_slopes || m->window > 0 || m->prefix_lens || m->row_begin);
+}
+
 rcp_status run_attention(rcp_cache* c, const void* q, const int32_t* cu_chunk, int32_t nq,
                          const int32_t* block_table, int32_t max_blocks_per_seq,
                          const int32_t* seq_lens, int32_t batch, void* out, void* ws,
                          size_t ws_size, rcp_stream stream, const AppendArgs* app = nullptr,
-                         bool recon = false, const SparseArgs* sparse = nullptr) {
+                         bool recon = false, const SparseArgs* sparse = nullptr,
+                         const rcp_score_mod* mod = nullptr) {
   if (!c || batch < 0 || nq < 0 || max_blocks_per_seq < 1) return RCP_ERR_INVALID_ARG;
   if (app && check_append(*app) != RCP_OK) return RCP_ERR_INVALID_ARG;
+  if (mod && (check_mod(*mod) != RCP_OK || max_blocks_per_seq > kMaxTableWidth))
+    return RCP_ERR_INVALID_ARG;
   if (nq == 0) {
     // nothing to attend; a step still appends its tokens
     if (!app || app->T == 0) return RCP_OK;
@@ -364,6 +412,16 @@ rcp_status run_attention(rcp_cache* c, const void* q, const int32_t* cu_chunk, i
   p.skip_tau = sparse ? sparse->tau : 0.f;
   p.page_kept = sparse ? sparse->page_kept : nullptr;
   p.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c->cfg.head_dim)));
+  if (modifies(mod)) {
+    const double log2e = 1.4426950408889634;
+    p.mod = 1;
+    p.window = mod->window;
+    p.cap2 = static_cast<float>(mod->softcap * log2e);
+    p.inv_cap2 = mod->softcap > 0.f ? static_cast<float>(1.0 / (mod->softcap * log2e)) : 0.f;
+    p.slopes = mod->alibi_slopes;
+    p.prefix_lens = mod->prefix_lens;
+    p.row_begin = mod->row_begin;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c->shape == kShapeMain) fill_ws<ShapeMain>(p, ws, nq);
@@ -553,6 +611,7 @@ rcp_status rcp_create_cache(const rcp_cache_config* cfg, void* k_pages, void* v_
   try {
     c->free_ids.resize(static_cast<size_t>(cfg->num_blocks));
     c->is_free.assign(static_cast<size_t>(cfg->num_blocks), 1);
+    c->refs.assign(static_cast<size_t>(cfg->num_blocks), 0);
   } catch (...) {
     delete c;
     return RCP_ERR_CAPACITY;
@@ -577,6 +636,7 @@ rcp_status rcp_alloc_blocks(rcp_cache* c, int32_t n, int32_t* ids_out) {
     const int32_t id = c->free_ids.back();
     c->free_ids.pop_back();
     c->is_free[static_cast<size_t>(id)] = 0;
+    c->refs[static_cast<size_t>(id)] = 1;
     ids_out[i] = id;
   }
   return RCP_OK;
@@ -599,10 +659,115 @@ rcp_status rcp_free_blocks(rcp_cache* c, int32_t n, const int32_t* ids) {
     }
   }
   for (int32_t i = 0; i < n; ++i) {
+    if (--c->refs[static_cast<size_t>(ids[i])] > 0) continue;   // a fork still holds it
     c->is_free[static_cast<size_t>(ids[i])] = 1;
     c->free_ids.push_back(ids[i]);
   }
   return RCP_OK;
+}
+
+rcp_status rcp_fork_blocks(rcp_cache* c, int32_t n, const int32_t* ids) {
+  if (!c || n < 0 || (n > 0 && !ids)) return RCP_ERR_INVALID_ARG;
+  const rcp_status st = check_forkable(c, n, ids, n);
+  if (st != RCP_OK) return st;
+  for (int32_t i = 0; i < n; ++i) ++c->refs[static_cast<size_t>(ids[i])];
+  return RCP_OK;
+}
+
+rcp_status rcp_block_refs(const rcp_cache* c, int32_t n, const int32_t* ids, int32_t* refs_out) {
+  if (!c || n < 0 || (n > 0 && (!ids || !refs_out))) return RCP_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (ids[i] < 0 || ids[i] >= c->cfg.num_blocks) return RCP_ERR_CAPACITY;
+  for (int32_t i = 0; i < n; ++i) refs_out[i] = c->refs[static_cast<size_t>(ids[i])];
+  return RCP_OK;
+}
+
+rcp_status rcp_fork_sequence(rcp_cache* c, const int32_t* ids, int32_t num_blocks, int32_t length,
+                             int32_t num_children, int32_t* child_ids, rcp_stream stream) {
+  if (!c || num_blocks < 0 || length < 0 || num_children < 0) return RCP_ERR_INVALID_ARG;
+  const int32_t full = length / rcp::kBlockSize, tail = length % rcp::kBlockSize ? 1 : 0;
+  if (full + tail > num_blocks) return RCP_ERR_INVALID_ARG;
+  if (full + tail == 0 || num_children == 0) return RCP_OK;
+  if (!ids || !child_ids) return RCP_ERR_INVALID_ARG;
+  // everything is checked before anything changes
+  rcp_status st = check_forkable(c, full + tail, ids, static_cast<int64_t>(full) * num_children);
+  if (st != RCP_OK) return st;
+  if (tail && static_cast<size_t>(num_children) > c->free_ids.size()) return RCP_ERR_CAPACITY;
+  if (tail && (st = ensure_device(c)) != RCP_OK) return st;
+  const int32_t stride = full + tail;
+  for (int32_t i0 = 0; tail && i0 < num_children; i0 += rcp::kCopyListMax) {
+    int32_t list[rcp::kCopyListMax];
+    rcp::CopyParams p{};
+    p.k_pages = c->k_pages;
+    p.v_pages = c->v_pages;
+    p.dev_err = c->dev_err;
+    p.num_blocks = c->cfg.num_blocks;
+    p.n = num_children - i0 < rcp::kCopyListMax ? num_children - i0 : rcp::kCopyListMax;
+    p.src = ids[full];
+    // the blocks the pool hands out next, taken once every copy is queued
+    for (int32_t i = 0; i < p.n; ++i)
+      list[i] = c->free_ids[c->free_ids.size() - 1 - static_cast<size_t>(i0 + i)];
+    if (copy_pages(c, p, list, stream) != cudaSuccess) return RCP_ERR_CUDA;
+  }
+  for (int32_t i = 0; i < num_children; ++i) {
+    int32_t* out = child_ids + static_cast<size_t>(i) * stride;
+    for (int32_t j = 0; j < full; ++j) {
+      ++c->refs[static_cast<size_t>(ids[j])];
+      out[j] = ids[j];
+    }
+    if (tail) rcp_alloc_blocks(c, 1, out + full);
+  }
+  return RCP_OK;
+}
+
+rcp_status rcp_copy_blocks(rcp_cache* c, const int32_t* pairs, int32_t num_pairs,
+                           rcp_stream stream) {
+  if (!c || num_pairs < 0) return RCP_ERR_INVALID_ARG;
+  if (num_pairs == 0) return RCP_OK;
+  if (!pairs || (reinterpret_cast<uintptr_t>(pairs) & 3u)) return RCP_ERR_INVALID_ARG;
+  const rcp_status st = ensure_device(c);
+  if (st != RCP_OK) return st;
+  rcp::CopyParams p{};
+  p.k_pages = c->k_pages;
+  p.v_pages = c->v_pages;
+  p.pairs = pairs;
+  p.dev_err = c->dev_err;
+  p.num_blocks = c->cfg.num_blocks;
+  p.n = num_pairs;
+  return copy_pages(c, p, nullptr, stream) == cudaSuccess ? RCP_OK : RCP_ERR_CUDA;
+}
+
+rcp_status rcp_compact_tokens(rcp_cache* c, const int32_t* block_table, int32_t max_blocks_per_seq,
+                              const int32_t* seq_lens, const uint8_t* keep, int32_t batch,
+                              int32_t* new_lens, rcp_stream stream) {
+  if (!c || batch < 0 || max_blocks_per_seq < 1 || max_blocks_per_seq > kMaxTableWidth)
+    return RCP_ERR_INVALID_ARG;
+  if (batch == 0) return RCP_OK;
+  if (!block_table || !seq_lens || !keep || !new_lens) return RCP_ERR_INVALID_ARG;
+  const uintptr_t in = reinterpret_cast<uintptr_t>(seq_lens), out = reinterpret_cast<uintptr_t>(new_lens);
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (in & 3u) || (out & 3u) || !aligned16(keep))
+    return RCP_ERR_INVALID_ARG;
+  // the lengths are read by every CTA of a request while one of them writes the new one
+  if ((in > out ? in - out : out - in) < static_cast<uintptr_t>(batch) * 4) return RCP_ERR_INVALID_ARG;
+  if (batch > kMaxCompactBatch) return RCP_ERR_UNSUPPORTED;
+  const rcp_status st = ensure_device(c);
+  if (st != RCP_OK) return st;
+  rcp::CompactParams p{};
+  p.k_pages = c->k_pages;
+  p.v_pages = c->v_pages;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.keep = keep;
+  p.new_lens = new_lens;
+  p.dev_err = c->dev_err;
+  p.num_blocks = c->cfg.num_blocks;
+  p.bt_stride = max_blocks_per_seq;
+  p.batch = batch;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = c->shape == kShapeMain
+                            ? rcp::launch_compact<ShapeMain>(p, c->cfg.page_format, s)
+                            : rcp::launch_compact<ShapeTiny>(p, c->cfg.page_format, s);
+  return e == cudaSuccess ? RCP_OK : RCP_ERR_CUDA;
 }
 
 rcp_status rcp_num_free_blocks(const rcp_cache* c, int64_t* n_free) {
@@ -637,6 +802,19 @@ rcp_status rcp_decode_step(rcp_cache* c, const void* k, const void* v, const int
   const AppendArgs app{k, v, slot_mapping, num_tokens};
   return run_attention(c, q, nullptr, batch, block_table, max_blocks_per_seq, seq_lens, batch, out,
                        workspace, workspace_bytes, stream, &app);
+}
+
+rcp_status rcp_decode_step_mod(rcp_cache* c, const void* k, const void* v,
+                               const int64_t* slot_mapping, int32_t num_tokens, const void* q,
+                               const int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t batch, const rcp_score_mod* mod,
+                               void* out, void* workspace, size_t workspace_bytes,
+                               rcp_stream stream) {
+  if (!c || batch < 0 || num_tokens < 0 || max_blocks_per_seq < 1) return RCP_ERR_INVALID_ARG;
+  const AppendArgs app{k, v, slot_mapping, num_tokens};
+  return run_attention(c, q, nullptr, batch, block_table, max_blocks_per_seq, seq_lens, batch, out,
+                       workspace, workspace_bytes, stream, num_tokens > 0 ? &app : nullptr, false,
+                       nullptr, mod);
 }
 
 rcp_status rcp_decode_attn(rcp_cache* c, const void* q, const int32_t* block_table,
@@ -694,6 +872,21 @@ rcp_status rcp_prefill_step(rcp_cache* c, const void* k, const void* v,
   return run_attention(c, q, cu_chunk_lens, num_query_rows, block_table, max_blocks_per_seq,
                        seq_lens, batch, out, workspace, workspace_bytes, stream, &app,
                        reconstruct != 0);
+}
+
+rcp_status rcp_prefill_step_mod(rcp_cache* c, const void* k, const void* v,
+                                const int64_t* slot_mapping, int32_t num_tokens, const void* q,
+                                const int32_t* cu_chunk_lens, int32_t num_query_rows,
+                                const int32_t* block_table, int32_t max_blocks_per_seq,
+                                const int32_t* seq_lens, int32_t batch, int32_t reconstruct,
+                                const rcp_score_mod* mod, void* out, void* workspace,
+                                size_t workspace_bytes, rcp_stream stream) {
+  if (!cu_chunk_lens || num_tokens < 0 || (reconstruct != 0 && reconstruct != 1))
+    return RCP_ERR_INVALID_ARG;
+  const AppendArgs app{k, v, slot_mapping, num_tokens};
+  return run_attention(c, q, cu_chunk_lens, num_query_rows, block_table, max_blocks_per_seq,
+                       seq_lens, batch, out, workspace, workspace_bytes, stream,
+                       num_tokens > 0 ? &app : nullptr, reconstruct != 0, nullptr, mod);
 }
 
 rcp_status rcp_prefill_reconstruct_workspace_size(const rcp_cache* c, int32_t max_query_rows,

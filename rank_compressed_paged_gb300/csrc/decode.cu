@@ -42,6 +42,7 @@
 #include "launch.h"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "scoremod.cuh"
 #include "shape.h"
 
 namespace rcp {
@@ -98,6 +99,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
         for (int32_t i = tid & 31; i < n; i += 32) {
           p.qlen[c0 + i] = L - n + i + 1;   // causal: row i sees keys 0 .. P + i
           p.qrow[c0 + i] = b;
+        }
+        if (p.vmap != nullptr) {
+          // score modifications: the prefix and the least first token of the request's rows
+          int32_t lo = INT32_MAX;   // none sees a token behind the prefix
+          for (int32_t i = tid & 31; i < n; i += 32) {
+            const int32_t pos = L - n + i, f = view_begin(p, c0 + i, pos);
+            if (f <= pos && f < lo) lo = f;
+          }
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          if ((tid & 31) == 0) {
+            p.vmap[2 * b] = view_prefix(p, b, L);
+            p.vmap[2 * b + 1] = lo;
+          }
         }
       }
     }
@@ -173,9 +187,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
         // reconstructing prefill: pages of every request with chunk rows, in request
         // order (the rows of V^)
         __syncthreads();
+        // (score modifications: the pages of the key tiles that some row sees)
+        auto pages_of = [&](int b) {
+          const int32_t nblk = (p.seq_lens[b] + kBlockSize - 1) / kBlockSize;
+          return p.vmap ? TileMap<S>(p.vmap + 2 * b, nblk).pages() : nblk;
+        };
         int64_t vs = 0;
         for (int b = b0; b < b1; ++b)
-          if (tiles_of(b) > 0) vs += (p.seq_lens[b] + kBlockSize - 1) / kBlockSize;
+          if (tiles_of(b) > 0) vs += pages_of(b);
         int64_t vin = vs;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
         for (int i = 0; i < w; ++i) v0 += warp_sum[i];
         if (tid == 0) p.vcum[0] = 0;
         for (int b = b0; b < b1; ++b) {
-          if (tiles_of(b) > 0) v0 += (p.seq_lens[b] + kBlockSize - 1) / kBlockSize;
+          if (tiles_of(b) > 0) v0 += pages_of(b);
           p.vcum[b + 1] = v0;
         }
       }
@@ -344,11 +363,18 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t codes) {
 }
 
 
+// Whether token t of a page is attended: the page's first nvalid tokens, or (BITS) those whose
+// bit is set.
+template <bool BITS>
+__device__ __forceinline__ bool token_ok(int nvalid, int t) {
+  return BITS ? (nvalid >> t) & 1 : t < nvalid;
+}
+
 // E4M3 pages, an even number of boxes: as widen_v_boxes below, in units of 16 codes (one
 // 16-byte load, two 16-byte stores).  A warp's 32 units are 4 tokens x 2 adjacent boxes x 4
 // units, so its loads cover four 128-byte row pieces and its stores eight 128-byte stage
 // rows: no shared-memory bank is hit twice beyond the minimum.
-template <class S, int NT>
+template <class S, int NT, bool BITS>
 __device__ __forceinline__ void widen_v_e4m3_pairs(const uint8_t* src, uint8_t* vb, int nvalid,
                                                    int b0, int b1, int tid) {
   const int n = (b1 - b0) * kBlockSize * 4;
@@ -357,7 +383,7 @@ __device__ __forceinline__ void widen_v_e4m3_pairs(const uint8_t* src, uint8_t* 
     const int c16 = idx & 3, gl = (idx >> 2) & 1, tl = (idx >> 3) & 3, th = (idx >> 5) & 3;
     const int tt = th * 4 + tl, gb = b0 + (idx >> 7) * 2 + gl;
     uint4 lo = make_uint4(0, 0, 0, 0), hi = make_uint4(0, 0, 0, 0);
-    if (tt < nvalid) {
+    if (token_ok<BITS>(nvalid, tt)) {
       const uint4 raw = *reinterpret_cast<const uint4*>(src + tt * S::R + gb * 64 + c16 * 16);
       lo.x = e4m3x2_to_half2_bits(static_cast<uint16_t>(raw.x & 0xFFFFu));
       lo.y = e4m3x2_to_half2_bits(static_cast<uint16_t>(raw.x >> 16));
@@ -376,7 +402,7 @@ __device__ __forceinline__ void widen_v_e4m3_pairs(const uint8_t* src, uint8_t* 
 
 // 4-bit pages, an even number of boxes: as widen_v_boxes below, in units of 16 codes (8 code
 // bytes, one scale), mapped to lanes like widen_v_e4m3_pairs.
-template <class S, int NT>
+template <class S, int NT, bool BITS>
 __device__ __forceinline__ void widen_v_int4_pairs(const uint8_t* src, uint8_t* vb, int nvalid,
                                                    int b0, int b1, int tid) {
   const int n = (b1 - b0) * kBlockSize * 4;
@@ -386,7 +412,7 @@ __device__ __forceinline__ void widen_v_int4_pairs(const uint8_t* src, uint8_t* 
     const int c16 = idx & 3, gl = (idx >> 2) & 1, tl = (idx >> 3) & 3, th = (idx >> 5) & 3;
     const int tt = th * 4 + tl, gb = b0 + (idx >> 7) * 2 + gl;
     uint4 lo = make_uint4(0, 0, 0, 0), hi = make_uint4(0, 0, 0, 0);
-    if (tt < nvalid) {
+    if (token_ok<BITS>(nvalid, tt)) {
       const uint2 raw =
           *reinterpret_cast<const uint2*>(src + tt * (S::R / 2) + gb * 32 + c16 * 8);
       const __half2 sc = __half2half2(scales[tt * (S::R / 64) + gb]);
@@ -409,17 +435,18 @@ __device__ __forceinline__ void widen_v_int4_pairs(const uint8_t* src, uint8_t* 
 // 4-bit: [16][R/2] code bytes then the fp16 scales [16][R/64]) into the fp16 stage vb in
 // the layout of the value MMA: box g at g * 2048, token row t at t * 128, 16-byte chunk c
 // at chunk c ^ (t % 8).  Tokens at or past nvalid (the sequence end, or a rejected block)
-// get zero rows, so whatever those slots hold cannot reach the accumulator through 0 * NaN.
+// get zero rows, so whatever those slots hold cannot reach the accumulator through 0 * NaN
+// (BITS: nvalid holds a bit per attended token).
 // NT threads, this one is tid.
-template <class S, int FMT, int NT>
+template <class S, int FMT, int NT, bool BITS = false>
 __device__ __forceinline__ void widen_v_boxes(const uint8_t* src, uint8_t* vb, int nvalid, int b0,
                                               int b1, int tid) {
   if constexpr (FMT == RCP_PAGES_FP8_E4M3 && S::NBOX % 2 == 0) {
-    widen_v_e4m3_pairs<S, NT>(src, vb, nvalid, b0, b1, tid);
+    widen_v_e4m3_pairs<S, NT, BITS>(src, vb, nvalid, b0, b1, tid);
     return;
   }
   if constexpr (FMT == RCP_PAGES_INT4 && S::NBOX % 2 == 0) {
-    widen_v_int4_pairs<S, NT>(src, vb, nvalid, b0, b1, tid);
+    widen_v_int4_pairs<S, NT, BITS>(src, vb, nvalid, b0, b1, tid);
     return;
   }
   const int n = (b1 - b0) * kBlockSize * 8;
@@ -427,7 +454,7 @@ __device__ __forceinline__ void widen_v_boxes(const uint8_t* src, uint8_t* vb, i
   for (int idx = tid; idx < n; idx += NT) {
     const int c = idx & 7, tt = (idx >> 3) % kBlockSize, gb = b0 + (idx >> 3) / kBlockSize;
     uint4 o = make_uint4(0, 0, 0, 0);
-    if (tt < nvalid) {
+    if (token_ok<BITS>(nvalid, tt)) {
       if constexpr (FMT == RCP_PAGES_INT4) {
         // box gb is exactly scale group gb: 8 codes (4 bytes) per 16-byte output chunk
         const uint32_t raw = *reinterpret_cast<const uint32_t*>(src + tt * (S::R / 2) + gb * 32 + c * 4);
@@ -548,31 +575,62 @@ __device__ __forceinline__ int32_t valid_len(int32_t L, int32_t max_len) {
   return (L >= 0 && L <= max_len) ? L : 0;
 }
 
+// The pages of request b that a decode reads, in order: all of them, or (MOD) the prefix's
+// pages and then those from the page of its first token behind the prefix on.
+template <bool MOD>
+struct ReqPages {
+  int32_t L, np, lp, total;   // tokens; prefix pages, page of the rest's start, pages
+  int32_t pfx, lo;            // MOD: the tokens seen are t < pfx and lo <= t < L
+  __device__ __forceinline__ ReqPages() {}
+  __device__ __forceinline__ ReqPages(const AttnParams& p, int b, int32_t max_len) {
+    L = valid_len(p.seq_lens[b], max_len);
+    total = (L + kBlockSize - 1) / kBlockSize;
+    if constexpr (MOD) {
+      pfx = view_prefix(p, b, L);
+      lo = L > 0 ? view_begin(p, b, L - 1) : 0;
+      np = (pfx + kBlockSize - 1) / kBlockSize;
+      lp = lo < L ? lo / kBlockSize : total;
+      if (lp < np) lp = np;   // they share a page, or the prefix reaches into the rest
+    }
+  }
+  __device__ __forceinline__ int32_t count() const { return MOD ? np + (total - lp) : total; }
+  __device__ __forceinline__ int32_t page(int32_t j) const {
+    return !MOD || j < np ? j : lp + (j - np);
+  }
+  // tokens of page x that are attended: their number, or (MOD) a bit for each
+  __device__ __forceinline__ int tokens(int32_t x) const {
+    const int32_t left = L - x * kBlockSize;
+    if constexpr (!MOD) return left < kBlockSize ? left : kBlockSize;
+    const int32_t t0 = x * kBlockSize;
+    return static_cast<int>((column_bits(0, pfx, t0) | column_bits(lo, L, t0)) & 0xFFFFu);
+  }
+};
+
 // Walks the requests that a partition's block range crosses; request b covers blocks
-// [bstart, bend) of the concatenated list of all requests' blocks.
+// [bstart, bend) of the concatenated list of the blocks that all requests read.
+template <bool MOD>
 struct ReqWalker {
-  const int32_t* lens;
+  const AttnParams* p;
   int32_t max_len;
   int b;
   int64_t bstart, bend;
-  __device__ __forceinline__ int64_t nblk(int r) const {
-    return (valid_len(lens[r], max_len) + kBlockSize - 1) / kBlockSize;
-  }
-  __device__ __forceinline__ void init(const int32_t* l, int32_t ml, int b0, int64_t s0) {
-    lens = l;
+  ReqPages<MOD> r;
+  __device__ __forceinline__ void init(const AttnParams& pp, int32_t ml, int b0, int64_t s0) {
+    p = &pp;
     max_len = ml;
     b = b0;
     bstart = s0;
-    bend = s0 + nblk(b0);
+    r = ReqPages<MOD>(pp, b0, ml);
+    bend = s0 + r.count();
   }
   __device__ __forceinline__ void advance_to(int64_t g) {
     while (g >= bend) {
       ++b;
       bstart = bend;
-      bend += nblk(b);
+      r = ReqPages<MOD>(*p, b, max_len);
+      bend += r.count();
     }
   }
-  __device__ __forceinline__ int32_t len() const { return valid_len(lens[b], max_len); }
 };
 
 // Blocks a decode step's append writes, as an open-addressing set in shared memory.
@@ -581,15 +639,17 @@ __device__ __forceinline__ uint32_t block_hash(int64_t blk) {
 }
 
 struct BlockInfo {
-  int nvalid;      // tokens of this block that are attended (0 for a rejected block id)
+  int nvalid;      // tokens of this block that are attended (0 for a rejected block id; MOD:
+                   // a bit per token)
   bool seg_first, seg_last;
 };
 
 
-template <class S, int FMT, bool SKIP>
+template <class S, int FMT, bool SKIP, bool MOD>
 __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
     decode_main_kernel(const __grid_constant__ CUtensorMap tmap_v,
-                       const __grid_constant__ CUtensorMap tmap_k, const AttnParams p) {
+                       const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ AttnParams p) {
   constexpr bool F8 = FMT != RCP_PAGES_FP16;   // quantized pages (E4M3 or 4-bit)
   // fp16 key pages with 128-byte rows (r_k = 64) arrive 128-byte swizzled (two TMA boxes of
   // 256 rows): chunk c of row r sits at chunk c ^ (r % 8), so the 16 lanes scoring one
@@ -737,7 +797,7 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
   {
     int64_t part = 0;
     for (int b = threadIdx.x; b < p.nq; b += NTHR)
-      part += (valid_len(p.seq_lens[b], max_len) + kBlockSize - 1) / kBlockSize;
+      part += ReqPages<MOD>(p, b, max_len).count();
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == 0) red[warp] = part;
@@ -776,7 +836,7 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
       if (b < p.nq) {
         const int32_t Lb = p.seq_lens[b];
         if (writer && (Lb < 0 || Lb > max_len)) atomicOr(p.dev_err, RCP_DEVERR_BAD_LEN);
-        v = (valid_len(Lb, max_len) + kBlockSize - 1) / kBlockSize;
+        v = ReqPages<MOD>(p, b, max_len).count();
       }
       int64_t incl = v;
 #pragma unroll
@@ -847,8 +907,8 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
   if (warp == 0 && lane == 0) prefetch_tmap(&tmap_v);
   griddep_launch();   // the combine + up-projection may start its prologue
 
-  ReqWalker walk;
-  if (active) walk.init(p.seq_lens, max_len, b_first, s_first);
+  ReqWalker<MOD> walk;
+  if (active) walk.init(p, max_len, b_first, s_first);
 
   if (!active) {
     // no blocks for this CTA
@@ -859,20 +919,19 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
     // load; lane 0 issues the copies.
     int* pg_phys = reinterpret_cast<int*>(sm + L::PG_OFF);   // [2][32]
     int* pg_nval = pg_phys + 64;                              // [2][32]
-    ReqWalker lw = walk;
+    ReqWalker<MOD> lw = walk;
     auto lookup = [&](int64_t gb, int& ph, int& nv) {
       const int64_t g = gb + lane;
       ph = 0;
       nv = 0;
       if (g < g1) {
         lw.advance_to(g);
-        const int64_t j = g - lw.bstart;
+        const int32_t j = lw.r.page(static_cast<int32_t>(g - lw.bstart));
         const int64_t raw = p.block_table[static_cast<int64_t>(lw.b) * p.bt_stride + j];
         const bool bad = raw < 0 || raw >= p.num_blocks;
         if (bad) atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
         ph = bad ? 0 : static_cast<int>(raw);
-        const int64_t left = lw.len() - j * kBlockSize;
-        nv = bad ? 0 : static_cast<int>(left < kBlockSize ? left : kBlockSize);
+        nv = bad ? 0 : lw.r.tokens(j);
       }
     };
     {
@@ -983,7 +1042,7 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
       }
       // TSC: the scores of page it + 1 go out before the values of page it, so that the
       // compute warps find the next page's scores ready when they finish this one
-      ReqWalker wsc = walk;   // the scoring MMAs' own walk, one page ahead
+      ReqWalker<MOD> wsc = walk;   // the scoring MMAs' own walk, one page ahead
       int64_t nseg = 0;       // segments whose scoring has started
       auto issue_scores = [&](int64_t g, int64_t it) -> bool {
         wsc.advance_to(g);
@@ -1149,7 +1208,7 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
     // boxes [0, WB) here; the compute warps widen the rest after writing P
     const int vt = threadIdx.x - 32 * (2 + NCW);   // 0 .. 32 NWW - 1
     const bool q_builder = vt < 64;                  // TSC: warps NCW+2, NCW+3
-    ReqWalker wq = walk;   // TSC: these warps also write each segment's query operand
+    ReqWalker<MOD> wq = walk;   // TSC: these warps also write each segment's query operand
     int64_t nseg = 0;
     bool q_ready = false;
     // SKIP: the kept pages, in order, until a stage whose info word is -1
@@ -1220,8 +1279,8 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
       bool ok = mbar_wait(&vfull[vr], (it / VRS) & 1, abort_flag, p.dev_err);
       if (it >= VST) ok = mbar_wait(&vfree[vs], ((it / VST) - 1) & 1, abort_flag, p.dev_err) && ok;
       if (!__all_sync(0xffffffffu, ok)) break;
-      widen_v_boxes<S, FMT, 32 * NWW>(vraw + vr * L::VPS, vst + vs * S::VSTAGE_BYTES, vinfo[vr], 0,
-                                      WB, vt);
+      widen_v_boxes<S, FMT, 32 * NWW, MOD>(vraw + vr * L::VPS, vst + vs * S::VSTAGE_BYTES,
+                                           vinfo[vr], 0, WB, vt);
       fence_proxy_async_smem();   // generic stores -> the MMA's async-proxy reads
       __syncwarp();
       if (lane == 0) {
@@ -1256,6 +1315,10 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
     };
     static_assert(!TSC || S::H == 8 * ROUNDS * (NCW / 4), "tensor scoring head split");
     float qf[ROUNDS];   // TSC: the segment's score factors 2^-e_h of this lane's heads
+    float slope2[ROUNDS];   // MOD: distance bias per token of this lane's heads, log2 units
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+      slope2[r] = MOD && p.slopes != nullptr && head_ok(r) ? p.slopes[head_of(r)] * 1.44269504f : 0.f;
     int64_t nseg_c = 0;
     int64_t kk = 0;     // pages accumulated so far (SKIP: the kept ones), orders P / V use
     int64_t nd = 0;     // SKIP: decisions posted to the value-copy warp
@@ -1427,6 +1490,19 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
       if (lane == 0) mbar_arrive(&kempty[ks]);
       }   // scores on the CUDA cores
 
+      if constexpr (MOD) {
+        // the cap, then the bias of this lane's token (four of each per page and lane: the
+        // page's scoring products outweigh them)
+        const int32_t tok = walk.r.page(static_cast<int32_t>(g - walk.bstart)) * kBlockSize + t;
+        const int32_t org = bias_origin(RowView{walk.r.pfx, walk.r.lo}, walk.r.L - 1);
+        const float dist = fabsf(static_cast<float>(org - tok));
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+          if (p.cap2 > 0.f) s[r] = cap_score(s[r], p.cap2, p.inv_cap2);
+          s[r] = fmaf(-slope2[r], dist, s[r]);
+        }
+      }
+
       // online softmax (base 2), lazy rescale: the reference max only moves when a block
       // max exceeds it by more than kRescaleThreshold, so the accumulator is rarely touched
       // The ROUNDS independent butterflies advance level by level, so their shuffle
@@ -1437,7 +1513,7 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
       bool need_any = false;
 #pragma unroll
       for (int r = 0; r < ROUNDS; ++r) {
-        valid[r] = ok && head_ok(r) && t < bi.nvalid;
+        valid[r] = ok && head_ok(r) && token_ok<MOD>(bi.nvalid, t);
         sv[r] = valid[r] ? s[r] : -INFINITY;
         bmax[r] = sv[r];
       }
@@ -1574,12 +1650,25 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
         // MMA that read it two blocks ago)
         const int vr = static_cast<int>(it % VRS);
         ok = mbar_wait(&vfull[vr], (it / VRS) & 1, abort_flag, p.dev_err) && ok;
-        widen_v_boxes<S, FMT, CT>(vraw + vr * L::VPS, vst + static_cast<int>(it % VST) * S::VSTAGE_BYTES,
-                             bi.nvalid, WB, S::NBOX, ctid);
+        widen_v_boxes<S, FMT, CT, MOD>(vraw + vr * L::VPS,
+                                       vst + static_cast<int>(it % VST) * S::VSTAGE_BYTES, bi.nvalid,
+                                       WB, S::NBOX, ctid);
         __syncwarp();
         if (lane == 0) mbar_arrive(&vempty[vr]);
       }
-      if (!F8 && bi.nvalid < kBlockSize) {
+      if (MOD && !F8 && bi.nvalid != 0xFFFF) {
+        // the same for the tokens of the page that the row does not see
+        const int vs = static_cast<int>(pi % VST);
+        ok = mbar_wait(&vfull[vs], (pi / VST) & 1, abort_flag, p.dev_err) && ok;
+        uint8_t* vb = vst + vs * S::VSTAGE_BYTES;
+        for (int idx = ctid; idx < kBlockSize * S::NBOX * 8; idx += CT) {
+          const int row = idx / (S::NBOX * 8), rem = idx % (S::NBOX * 8);
+          if (!token_ok<true>(bi.nvalid, row))
+            *reinterpret_cast<uint4*>(vb + (rem >> 3) * 2048 + row * 128 + (rem & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (!MOD && !F8 && bi.nvalid < kBlockSize) {
         // tokens past the sequence end (or a rejected block): zero their V rows so that
         // whatever those slots hold cannot reach the accumulator through 0 * NaN
         const int vs = static_cast<int>(pi % VST);
@@ -1677,20 +1766,27 @@ cudaError_t prepare_attn(int device) {
   auto set = [](auto kernel, int smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
-  cudaError_t e = set(decode_main_kernel<S, RCP_PAGES_FP16, false>, DecodeSmem<S, RCP_PAGES_FP16>::ALLOC);
+  cudaError_t e = set(decode_main_kernel<S, RCP_PAGES_FP16, false, false>, DecodeSmem<S, RCP_PAGES_FP16>::ALLOC);
   if (e == cudaSuccess)
-    e = set(decode_main_kernel<S, RCP_PAGES_FP8_E4M3, false>,
+    e = set(decode_main_kernel<S, RCP_PAGES_FP8_E4M3, false, false>,
             DecodeSmem<S, RCP_PAGES_FP8_E4M3>::ALLOC);
   if (e == cudaSuccess)
-    e = set(decode_main_kernel<S, RCP_PAGES_INT4, false>, DecodeSmem<S, RCP_PAGES_INT4>::ALLOC);
+    e = set(decode_main_kernel<S, RCP_PAGES_INT4, false, false>, DecodeSmem<S, RCP_PAGES_INT4>::ALLOC);
   if (e == cudaSuccess)
-    e = set(decode_main_kernel<S, RCP_PAGES_FP16, true>,
+    e = set(decode_main_kernel<S, RCP_PAGES_FP16, true, false>,
             DecodeSmem<S, RCP_PAGES_FP16, true>::ALLOC);
   if (e == cudaSuccess)
-    e = set(decode_main_kernel<S, RCP_PAGES_FP8_E4M3, true>,
+    e = set(decode_main_kernel<S, RCP_PAGES_FP8_E4M3, true, false>,
             DecodeSmem<S, RCP_PAGES_FP8_E4M3, true>::ALLOC);
   if (e == cudaSuccess)
-    e = set(decode_main_kernel<S, RCP_PAGES_INT4, true>, DecodeSmem<S, RCP_PAGES_INT4, true>::ALLOC);
+    e = set(decode_main_kernel<S, RCP_PAGES_INT4, true, false>, DecodeSmem<S, RCP_PAGES_INT4, true>::ALLOC);
+  if (e == cudaSuccess)
+    e = set(decode_main_kernel<S, RCP_PAGES_FP16, false, true>, DecodeSmem<S, RCP_PAGES_FP16>::ALLOC);
+  if (e == cudaSuccess)
+    e = set(decode_main_kernel<S, RCP_PAGES_FP8_E4M3, false, true>,
+            DecodeSmem<S, RCP_PAGES_FP8_E4M3>::ALLOC);
+  if (e == cudaSuccess)
+    e = set(decode_main_kernel<S, RCP_PAGES_INT4, false, true>, DecodeSmem<S, RCP_PAGES_INT4>::ALLOC);
   return e;
 }
 
@@ -1708,20 +1804,27 @@ cudaError_t launch_attn(const CUtensorMap& tmap_v, const CUtensorMap& tmap_k, co
   auto go = [&](auto kernel, int threads, int smem) {
     return launch_pdl(kernel, dim3(p.parts), dim3(threads), smem, stream, pdl, tmap_v, tmap_k, p);
   };
-  if (p.page_format == E4M3)
-    e = p.sparse ? go(decode_main_kernel<S, E4M3, true>, decode_threads<S, E4M3, true>(),
+  if (p.mod)
+    e = p.page_format == E4M3 ? go(decode_main_kernel<S, E4M3, false, true>,
+                                   decode_threads<S, E4M3>(), DecodeSmem<S, E4M3>::ALLOC)
+        : p.page_format == I4 ? go(decode_main_kernel<S, I4, false, true>, decode_threads<S, I4>(),
+                                   DecodeSmem<S, I4>::ALLOC)
+                              : go(decode_main_kernel<S, F16, false, true>,
+                                   decode_threads<S, F16>(), DecodeSmem<S, F16>::ALLOC);
+  else if (p.page_format == E4M3)
+    e = p.sparse ? go(decode_main_kernel<S, E4M3, true, false>, decode_threads<S, E4M3, true>(),
                       DecodeSmem<S, E4M3, true>::ALLOC)
-                 : go(decode_main_kernel<S, E4M3, false>, decode_threads<S, E4M3>(),
+                 : go(decode_main_kernel<S, E4M3, false, false>, decode_threads<S, E4M3>(),
                       DecodeSmem<S, E4M3>::ALLOC);
   else if (p.page_format == I4)
-    e = p.sparse ? go(decode_main_kernel<S, I4, true>, decode_threads<S, I4, true>(),
+    e = p.sparse ? go(decode_main_kernel<S, I4, true, false>, decode_threads<S, I4, true>(),
                       DecodeSmem<S, I4, true>::ALLOC)
-                 : go(decode_main_kernel<S, I4, false>, decode_threads<S, I4>(),
+                 : go(decode_main_kernel<S, I4, false, false>, decode_threads<S, I4>(),
                       DecodeSmem<S, I4>::ALLOC);
   else
-    e = p.sparse ? go(decode_main_kernel<S, F16, true>, decode_threads<S, F16, true>(),
+    e = p.sparse ? go(decode_main_kernel<S, F16, true, false>, decode_threads<S, F16, true>(),
                       DecodeSmem<S, F16, true>::ALLOC)
-                 : go(decode_main_kernel<S, F16, false>, decode_threads<S, F16>(),
+                 : go(decode_main_kernel<S, F16, false, false>, decode_threads<S, F16>(),
                       DecodeSmem<S, F16>::ALLOC);
   if (e != cudaSuccess) return e;
   if (prof_stop && (e = cudaEventRecord(prof_stop, stream)) != cudaSuccess) return e;

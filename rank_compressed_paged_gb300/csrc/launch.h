@@ -62,4 +62,14 @@ cudaError_t launch_combine_upproj(const CUtensorMap& w_v_mn, const CUtensorMap& 
                                   const CUtensorMap& rec_ml, const CombineParams& p,
                                   cudaStream_t stream, bool pdl);
 
+// Page copies (pages.cu): p.n device pairs, or one source to the p.n <= kCopyListMax listed
+// destinations (a host array, passed by value).
+constexpr int kCopyListMax = 960;   // the kernel's parameters stay below 4 KiB
+template <class S>
+cudaError_t launch_copy_pages(const CopyParams& p, const int32_t* list, int page_format,
+                              int num_sms, cudaStream_t stream);
+// In-place compaction of every request's kept tokens (pages.cu).
+template <class S>
+cudaError_t launch_compact(const CompactParams& p, int page_format, cudaStream_t stream);
+
 }  // namespace rcp

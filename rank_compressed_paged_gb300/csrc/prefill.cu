@@ -36,6 +36,7 @@
 #include "launch.h"
 #include "ptx.cuh"
 #include "rcp.h"
+#include "scoremod.cuh"
 #include "shape.h"
 
 namespace rcp {
@@ -45,7 +46,7 @@ constexpr float kPfRescale = 8.f;   // log2 units: weights stay below 2^8 betwee
 
 // RECON: the values are the reconstructed V^ rows of head h (N = d) instead of a slice
 // of the joint coefficients (N = RQ), and the epilogue writes O directly.
-template <class S, bool RECON>
+template <class S, bool RECON, bool MOD = false>
 struct PfSmem {
   using C = PrefillCfg<S>;
   static constexpr int VN = RECON ? S::D : C::RQ;       // value MMA N
@@ -71,7 +72,11 @@ struct PfSmem {
   static constexpr int NBAR = 11 + 4 * NS;
   static constexpr int BAR_OFF = END;                   // NBAR mbarriers
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;   // tmem slot, abort flag
-  static constexpr int TOTAL = MISC_OFF + 16;
+  // MOD: least and largest first token of the tile's rows (per warp), the rejected pages of
+  // each key stage and of each score buffer, and the softmax warps' column masks [2][4][4]
+  static constexpr int MOD_OFF = MISC_OFF + 16;
+  static constexpr int MOD_BYTES = MOD ? (8 + 8 + 2 + 2 * 16) * 4 : 0;
+  static constexpr int TOTAL = MOD_OFF + MOD_BYTES;
   static constexpr int ALLOC = TOTAL + 1024;
   static constexpr int RPC = 128 / NQ;                  // output rows each slice CTA sums
   static constexpr int TMEM_COLS = pow2_at_least(256 + VN, 32);
@@ -81,15 +86,20 @@ struct PfSmem {
   static_assert(!RECON || P_TM + C::KT <= TMEM_COLS, "P buffers in tensor memory");
 };
 
-template <class S, bool RECON>
+// MOD: score modifications (rcp_score_mod).  A row sees keys t < pfx and lo <= t <= pos with
+// its own lo, so the CTA walks the key tiles of the prefix and those from the least lo of
+// its rows on; each row masks its scores to what it sees, and a key that no row of the tile
+// sees has its value row zeroed.
+template <class S, bool RECON, bool MOD>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qhi_map,
                    const __grid_constant__ CUtensorMap qlo_map,
                    const __grid_constant__ CUtensorMap kp_map,
                    const __grid_constant__ CUtensorMap vp_map,
-                   const __grid_constant__ CUtensorMap w_map, const AttnParams p) {
+                   const __grid_constant__ CUtensorMap w_map,
+                   const __grid_constant__ AttnParams p) {
   using C = PrefillCfg<S>;
-  using L = PfSmem<S, RECON>;
+  using L = PfSmem<S, RECON, MOD>;
   constexpr int KT = C::KT, RQ = C::RQ, NQ = L::NQ, NG = L::NG, VN = L::VN, D = S::D, H = S::H;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -123,9 +133,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int Lb = p.seq_lens[b], P0 = Lb - n;
   const int i0 = qt * 128;                              // first chunk row of this tile
   const int i_last = min(n, i0 + 128) - 1;
-  const int nkt = (P0 + i_last + 1 + KT - 1) / KT;      // key tiles (causal limit)
+  int nkt = (P0 + i_last + 1 + KT - 1) / KT;            // key tiles (causal limit)
   const int nblk = (Lb + kBlockSize - 1) / kBlockSize;
   const int row0 = c0 + i0;
+  int* wlo = reinterpret_cast<int*>(sm + L::MOD_OFF);   // MOD [8]: least, largest lo per warp
+  int* kbad = wlo + 8;                                  // MOD [8]: rejected pages of a tile
+  int* sbad = kbad + 8;                                 // MOD [2]: the same per score buffer
+  uint32_t* colm = reinterpret_cast<uint32_t*>(sbad + 2);   // MOD [2][4][4]
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -135,8 +149,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
+    mbar_init(&s_full[0], MOD ? 2 : 1);   // the commit (MOD: and the MMA thread, after sbad)
+    mbar_init(&s_full[1], MOD ? 2 : 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
@@ -152,10 +166,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tmem_alloc(tmem_slot, L::TMEM_COLS);
     tmem_relinquish();
   }
+  // MOD: rows of this tile by thread, their first tokens; rows past the chunk do not count
+  if constexpr (MOD) {
+    if (warp < 4) {
+      const int ci = i0 + static_cast<int>(threadIdx.x);
+      const int32_t f = ci < n ? view_begin(p, c0 + ci, P0 + ci) : 0;
+      const int32_t least = __reduce_min_sync(0xffffffffu, ci < n && f <= P0 + ci ? f : INT32_MAX);
+      const int32_t most = __reduce_max_sync(0xffffffffu, ci < n ? f : 0);
+      if (lane == 0) {
+        wlo[warp] = least;
+        wlo[4 + warp] = most;
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  int32_t pfx = 0, lo_min = 0, lo_max = 0, npt = 0, lt = 0;   // MOD: tiles [0, npt), then lt ..
+  if constexpr (MOD) {
+    pfx = view_prefix(p, b, Lb);
+    lo_min = min(min(wlo[0], wlo[1]), min(wlo[2], wlo[3]));
+    lo_max = max(max(wlo[4], wlo[5]), max(wlo[6], wlo[7]));
+    npt = (pfx + KT - 1) / KT;
+    lt = lo_min < INT32_MAX ? lo_min / KT : nkt;
+    lt = max(lt, npt);
+    nkt = npt + max(0, nkt - lt);
+  }
+  // key tile number j of this CTA
+  auto tile_of = [&](int j) { return MOD && j >= npt ? lt + (j - npt) : j; };
+  // whether page x of the request is read (MOD: some row of the tile may see it)
+  auto page_read = [&](int x) {
+    return x < nblk && (!MOD || x * kBlockSize < pfx || (x + 1) * kBlockSize > lo_min);
+  };
   if constexpr (NQ > 1) cluster_sync_all();   // peers are running before any remote store
 
   if (warp == 0) {
@@ -171,21 +214,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tma_load_2d(sm + L::Q_BYTES, &qlo_map, h * 64, row0, q_full);
     }
     const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-    int32_t nxt = (lane < BPT && lane < nblk) ? table[lane] : -1;
+    const int pg0 = tile_of(0) * BPT + lane;
+    int32_t nxt = (lane < BPT && nkt > 0 && page_read(pg0)) ? table[pg0] : -1;
     for (int j = 0; j < nkt; ++j) {
       const int s = j % NS;
-      const bool mine = lane < BPT && j * BPT + lane < nblk;
+      const bool mine = lane < BPT && page_read(tile_of(j) * BPT + lane);
       int32_t phys = mine ? nxt : -1;
       if (mine && (phys < 0 || phys >= p.num_blocks)) {
         atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
         phys = -1;
       }
-      const int nb = (j + 1) * BPT + lane;                 // the next tile's page, in flight
-      nxt = (lane < BPT && nb < nblk) ? table[nb] : -1;
+      const int nb = tile_of(j + 1) * BPT + lane;          // the next tile's page, in flight
+      nxt = (lane < BPT && j + 1 < nkt && page_read(nb)) ? table[nb] : -1;
+      // MOD: rejected pages, for the softmax to mask (keys run at most NS + 2 tiles ahead of it)
+      const uint32_t rejected = MOD ? __ballot_sync(0xffffffffu, mine && phys < 0) : 0;
       const int nload = __popc(__ballot_sync(0xffffffffu, phys >= 0));
       bool ok = true;
       if (lane == 0) {
         ok = j < NS || mbar_wait(&k_empty[s], ((j / NS) - 1) & 1, abort_flag, p.dev_err);
+        if constexpr (MOD) kbad[j & 7] = static_cast<int>(rejected);
         if (ok) mbar_arrive_expect_tx(&k_full[s], nload * 2048);
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;   // the byte count is armed first
@@ -204,7 +251,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           uint8_t* vst = sm + L::ST_OFF + s * L::STAGE + L::K_BYTES;
           if (j >= NS && !mbar_wait(&v_empty[s], ((j / NS) - 1) & 1, abort_flag, p.dev_err)) break;
           mbar_arrive_expect_tx(&v_full[s], NG * KT * 128);
-          const int64_t vrow = p.vcum[b] * kBlockSize + static_cast<int64_t>(j) * KT;
+          // MOD: V^ holds the tiles that some row of the request sees
+          const int vt = MOD ? TileMap<S>(p.vmap + 2 * b, nblk).compact(tile_of(j)) : j;
+          const int64_t vrow = p.vcum[b] * kBlockSize + static_cast<int64_t>(vt) * KT;
 #pragma unroll
           for (int g = 0; g < NG; ++g)
             tma_load_2d(vst + g * KT * 128, &vp_map, h * D + g * 64, static_cast<int32_t>(vrow),
@@ -217,14 +266,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       constexpr int BPT = KT / kBlockSize;
       if (lane == 0) prefetch_tmap(&vp_map);
       const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-      int32_t nxt = (lane < BPT && lane < nblk) ? table[lane] : -1;
+      const int pg0 = tile_of(0) * BPT + lane;
+      int32_t nxt = (lane < BPT && nkt > 0 && page_read(pg0)) ? table[pg0] : -1;
       for (int j = 0; j < nkt; ++j) {
         const int s = j % NS;
-        const bool mine = lane < BPT && j * BPT + lane < nblk;
+        const bool mine = lane < BPT && page_read(tile_of(j) * BPT + lane);
         const int32_t id = mine ? nxt : -1;
         const int32_t phys = (id >= 0 && id < p.num_blocks) ? id : -1;   // keys report bad ids
-        const int nb = (j + 1) * BPT + lane;
-        nxt = (lane < BPT && nb < nblk) ? table[nb] : -1;
+        const int nb = tile_of(j + 1) * BPT + lane;
+        nxt = (lane < BPT && j + 1 < nkt && page_read(nb)) ? table[nb] : -1;
         const int nload = __popc(__ballot_sync(0xffffffffu, phys >= 0));
         bool go = true;
         if (lane == 0) {
@@ -279,6 +329,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                      id_s, kk > 0 ? 1u : 0u);
             umma_f16(tmem + (js & 1) * 128,
                      make_sdesc(qa + L::Q_BYTES + kk * 32, 16, 1024, kSwizzle128B), bd, id_s, 1u);
+          }
+          if constexpr (MOD) {
+            sbad[js & 1] = kbad[js & 7];
+            mbar_arrive(&s_full[js & 1]);
           }
           umma_commit(&s_full[js & 1]);
           umma_commit(&k_empty[js % NS]);
@@ -351,6 +405,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int pos = P0 + ci;                            // keys 0 .. pos are attended
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float m_run = -INFINITY, l_run = 0.f;
+    // MOD: what this row sees, its head's bias per token (log2 units) and where it starts from
+    RowView view{pfx, 0};
+    int32_t org = 0;
+    float slope2 = 0.f;
+    if constexpr (MOD) {
+      view.lo = row_ok ? view_begin(p, row0 + r, pos) : 0;
+      org = bias_origin(view, pos);
+      slope2 = p.slopes ? p.slopes[h] * 1.44269504f : 0.f;
+    }
     uint8_t* pbuf = sm + L::P_OFF;
     for (int j = 0; j < nkt; ++j) {
       const int s = j & 1;
@@ -365,10 +428,54 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tmem_ld16(tl + s * 128 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
         tmem_wait_ld();
       }
-      const bool full_tile = __all_sync(0xffffffffu, lim >= KT - 1);   // below the diagonal
+      const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key
+      uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
+      if constexpr (MOD) {
+        if (ok && p.cap2 > 0.f) {
+#pragma unroll
+          for (int c = 0; c < KT; ++c) sv[c] = cap_score(sv[c], p.cap2, p.inv_cap2);
+        }
+        if (ok && p.slopes) {
+          const float d0 = static_cast<float>(org - t0);
+#pragma unroll
+          for (int c = 0; c < KT; ++c) sv[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
+        }
+        // a tile that every row of the CTA sees whole needs no mask
+        const uint32_t bad = static_cast<uint32_t>(sbad[s]);
+        const bool whole = bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
+        if (!ok || !row_ok || !whole) {
+#pragma unroll
+          for (int k = 0; k < KT / 32; ++k) {
+            uint32_t w = 0;
+            if (ok && row_ok) {
+              w = column_bits(0, view.pfx, t0 + 32 * k) | column_bits(view.lo, pos + 1, t0 + 32 * k);
+              if ((bad >> (2 * k)) & 1u) w &= 0xFFFF0000u;
+              if ((bad >> (2 * k)) & 2u) w &= 0x0000FFFFu;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sv[32 * k + c] = (w >> c) & 1u ? sv[32 * k + c] : -INFINITY;
+            unseen[k] = w;   // keys this row sees, until the rows are joined below
+          }
+        }
+        if (!whole) {   // uniform over the softmax warps
+          uint32_t* cm = colm + s * 16;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = __reduce_or_sync(0xffffffffu, unseen[k]);
+            if (lane == 0) cm[quarter * 4 + k] = w;
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) unseen[k] = 0;
+        }
+      }
+      const bool full_tile = MOD || __all_sync(0xffffffffu, lim >= KT - 1);   // below the diagonal
       // masked columns (diagonal tiles, rows past the chunk, a failed wait) become -inf, so
       // the max and the exponentials below need no per-element test (exp2(-inf) = 0)
-      if (!ok || !full_tile) {
+      if (!MOD && (!ok || !full_tile)) {
 #pragma unroll
         for (int c = 0; c < KT; ++c) sv[c] = (ok && c <= lim) ? sv[c] : -INFINITY;
       }
@@ -458,7 +565,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       l_run = l_run * alpha + rsum;
       m_run = m_new;
-      if (j * KT + KT > Lb) {
+      if (MOD && (unseen[0] | unseen[1] | unseen[2] | unseen[3])) {
+        // keys that no row sees (among them tokens past the end and rejected pages): the same
+        ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
+        uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
+        for (int idx = threadIdx.x - 64; idx < KT * NG * 8; idx += 128) {   // warps 2-5
+          const int tok = idx / (NG * 8);
+          const uint32_t w = tok < 64 ? (tok < 32 ? unseen[0] : unseen[1])
+                                      : (tok < 96 ? unseen[2] : unseen[3]);
+          if (!((w >> (tok & 31)) & 1u)) continue;
+          const int rem = idx % (NG * 8);
+          const int g = rem >> 3, ch = rem & 7;
+          *reinterpret_cast<uint4*>(vst + (g * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
+                                    (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (!MOD && j * KT + KT > Lb) {
         // tokens past the end of the request: zero their value rows so that whatever the
         // slots hold (or stale bytes of skipped pages) never meet a zero weight as 0 * NaN
         ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
@@ -493,6 +615,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           uint32_t w8[8];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
+            if (MOD && !(l_run > 0.f)) v[e] = v[e + 1] = 0.f;   // saw no key: no accumulator
             const __half2 hv = __floats2half2_rn(v[e] * inv, v[e + 1] * inv);
             w8[e / 2] = *reinterpret_cast<const uint32_t*>(&hv);
           }
@@ -520,6 +643,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         uint32_t hw[16], lw[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
+          if (MOD && !(l_run > 0.f)) v[e] = v[e + 1] = 0.f;   // saw no key: no accumulator
           const float z0 = v[e] * inv, z1 = v[e + 1] * inv;
           const __half2 hi = __floats2half2_rn(z0, z1);
           const float2 hb = __half22float2(hi);
@@ -627,12 +751,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 // --------------------------------------------------------------------------- launches
 template <class S>
 cudaError_t prepare_prefill() {
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<S, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       PfSmem<S, false>::ALLOC);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(prefill_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PfSmem<S, true>::ALLOC);
+  auto set = [](auto kernel, int smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  cudaError_t e = set(prefill_kernel<S, false, false>, PfSmem<S, false>::ALLOC);
+  if (e == cudaSuccess) e = set(prefill_kernel<S, true, false>, PfSmem<S, true>::ALLOC);
+  if (e == cudaSuccess) e = set(prefill_kernel<S, false, true>, PfSmem<S, false, true>::ALLOC);
+  if (e == cudaSuccess) e = set(prefill_kernel<S, true, true>, PfSmem<S, true, true>::ALLOC);
   return e;
 }
 
@@ -645,7 +770,8 @@ cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(max_tiles * S::H * NQ);
   cfg.blockDim = dim3(kPfThreads);
-  cfg.dynamicSmemBytes = recon ? PfSmem<S, true>::ALLOC : PfSmem<S, false>::ALLOC;
+  cfg.dynamicSmemBytes = p.mod ? (recon ? PfSmem<S, true, true>::ALLOC : PfSmem<S, false, true>::ALLOC)
+                               : (recon ? PfSmem<S, true>::ALLOC : PfSmem<S, false>::ALLOC);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   int na = 0;
@@ -661,8 +787,11 @@ cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const
   }
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  if (recon) return cudaLaunchKernelEx(&cfg, prefill_kernel<S, true>, qhi, qlo, kp, vp, w, p);
-  return cudaLaunchKernelEx(&cfg, prefill_kernel<S, false>, qhi, qlo, kp, vp, w, p);
+  if (p.mod)
+    return recon ? cudaLaunchKernelEx(&cfg, prefill_kernel<S, true, true>, qhi, qlo, kp, vp, w, p)
+                 : cudaLaunchKernelEx(&cfg, prefill_kernel<S, false, true>, qhi, qlo, kp, vp, w, p);
+  if (recon) return cudaLaunchKernelEx(&cfg, prefill_kernel<S, true, false>, qhi, qlo, kp, vp, w, p);
+  return cudaLaunchKernelEx(&cfg, prefill_kernel<S, false, false>, qhi, qlo, kp, vp, w, p);
 }
 
 template cudaError_t prepare_prefill<ShapeMain>();

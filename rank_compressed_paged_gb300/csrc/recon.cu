@@ -40,6 +40,7 @@
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "rcp.h"
+#include "scoremod.cuh"
 #include "shape.h"
 
 namespace rcp {
@@ -79,7 +80,8 @@ constexpr int recon_pairs() {
   return (S::H * S::D / ReconCfg<S>::NT) % 2 == 0 ? 2 : 1;
 }
 
-template <class S>
+// MOD (score modifications): the keys are those of the tiles that some row sees (TileMap).
+template <class S, bool MOD>
 __global__ void __launch_bounds__(kRcThreads, 1)
     recon_kernel(const __grid_constant__ CUtensorMap vp_map, const __grid_constant__ CUtensorMap w_map,
                  const AttnParams p) {
@@ -206,9 +208,16 @@ __global__ void __launch_bounds__(kRcThreads, 1)
             const int mid = (lo + hi) >> 1;
             if (p.vcum[mid] <= g) lo = mid; else hi = mid;
           }
-          const int32_t id = p.block_table[static_cast<int64_t>(lo) * p.bt_stride + (g - p.vcum[lo])];
+          int32_t j = static_cast<int32_t>(g - p.vcum[lo]);
+          bool seen = true;
+          if constexpr (MOD) {
+            const TileMap<S> m(p.vmap + 2 * lo, (p.seq_lens[lo] + kBlockSize - 1) / kBlockSize);
+            j = m.page(j);
+            seen = m.seen(j);   // another page of a tile that is: zeros
+          }
+          const int32_t id = seen ? p.block_table[static_cast<int64_t>(lo) * p.bt_stride + j] : -1;
           if (id >= 0 && id < p.num_blocks) y = id * kBlockSize;
-          else if (t % NU == 0) atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
+          else if (seen && t % NU == 0) atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
         }
         rows_s[r * 8 + lane] = y;
       }
@@ -269,8 +278,14 @@ __global__ void __launch_bounds__(kRcThreads, 1)
           const int mid = (lo + hi) >> 1;
           if (p.vcum[mid] <= g) lo = mid; else hi = mid;
         }
-        const int64_t blk = g - p.vcum[lo];
-        const int32_t id = p.block_table[static_cast<int64_t>(lo) * p.bt_stride + blk];
+        int64_t blk = g - p.vcum[lo];
+        bool seen = true;
+        if constexpr (MOD) {
+          const TileMap<S> m(p.vmap + 2 * lo, (p.seq_lens[lo] + kBlockSize - 1) / kBlockSize);
+          blk = m.page(static_cast<int32_t>(blk));
+          seen = m.seen(static_cast<int32_t>(blk));
+        }
+        const int32_t id = seen ? p.block_table[static_cast<int64_t>(lo) * p.bt_stride + blk] : -1;
         keep = id >= 0 && id < p.num_blocks && blk * kBlockSize + tok < p.seq_lens[lo];
       }
       // the row this lane stores in the copy-out: 4 rows per instruction, 8 lanes per row
@@ -341,7 +356,7 @@ __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t codes) {   // low byte
   return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
 }
 
-template <class S, int FMT>
+template <class S, int FMT, bool MOD>
 __global__ void __launch_bounds__(kWidenThreads)
     widen_pages_kernel(const AttnParams p, __half* k16, __half* v16, int32_t* table16) {
   constexpr bool I4 = FMT == RCP_PAGES_INT4;
@@ -366,11 +381,17 @@ __global__ void __launch_bounds__(kWidenThreads)
         const int mid = (lo + hi) >> 1;
         if (p.vcum[mid] <= g) lo = mid; else hi = mid;
       }
-      const int64_t j = g - p.vcum[lo];
+      int64_t j = g - p.vcum[lo];
+      bool seen = true;
+      if constexpr (MOD) {
+        const TileMap<S> m(p.vmap + 2 * lo, (p.seq_lens[lo] + kBlockSize - 1) / kBlockSize);
+        j = m.page(static_cast<int32_t>(j));
+        seen = m.seen(static_cast<int32_t>(j));
+      }
       const int64_t at = static_cast<int64_t>(lo) * p.bt_stride + j;
-      int64_t id = p.block_table[at];
+      int64_t id = seen ? p.block_table[at] : -1;
       if (id < 0 || id >= p.num_blocks) {
-        atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
+        if (seen) atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
         id = -1;
       }
       table16[at] = id < 0 ? -1 : static_cast<int32_t>(g);
@@ -426,17 +447,24 @@ cudaError_t launch_widen(const AttnParams& p, void* k16, void* v16, int32_t* tab
   if (max_pages <= 0) return cudaSuccess;
   const int64_t cap = static_cast<int64_t>(num_sms) * 8;   // grid-stride over the pages
   const unsigned grid = static_cast<unsigned>(max_pages < cap ? max_pages : cap);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(grid), dim3(kWidenThreads), 0, stream, pdl, p,
+                      static_cast<__half*>(k16), static_cast<__half*>(v16), table16);
+  };
   if (p.page_format == RCP_PAGES_INT4)
-    return launch_pdl(widen_pages_kernel<S, RCP_PAGES_INT4>, dim3(grid), dim3(kWidenThreads), 0,
-                      stream, pdl, p, static_cast<__half*>(k16), static_cast<__half*>(v16),
-                      table16);
-  return launch_pdl(widen_pages_kernel<S, RCP_PAGES_FP8_E4M3>, dim3(grid), dim3(kWidenThreads), 0,
-                    stream, pdl, p, static_cast<__half*>(k16), static_cast<__half*>(v16), table16);
+    return p.mod ? go(widen_pages_kernel<S, RCP_PAGES_INT4, true>)
+                 : go(widen_pages_kernel<S, RCP_PAGES_INT4, false>);
+  return p.mod ? go(widen_pages_kernel<S, RCP_PAGES_FP8_E4M3, true>)
+               : go(widen_pages_kernel<S, RCP_PAGES_FP8_E4M3, false>);
 }
 
 template <class S>
 cudaError_t prepare_recon() {
-  return cudaFuncSetAttribute(recon_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e =
+      cudaFuncSetAttribute(recon_kernel<S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           ReconSmem<S>::ALLOC);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(recon_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               ReconSmem<S>::ALLOC);
 }
 
@@ -466,7 +494,7 @@ cudaError_t launch_recon(const CUtensorMap& vp, const CUtensorMap& w_v_mn, const
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, recon_kernel<S>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, recon_kernel<S, false>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();   // a failed query leaves no error behind
       n = num_sms / CL;
     }
@@ -480,7 +508,8 @@ cudaError_t launch_recon(const CUtensorMap& vp, const CUtensorMap& w_v_mn, const
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, recon_kernel<S>, vp, w_v_mn, p);
+  if (p.mod) return cudaLaunchKernelEx(&cfg, recon_kernel<S, true>, vp, w_v_mn, p);
+  return cudaLaunchKernelEx(&cfg, recon_kernel<S, false>, vp, w_v_mn, p);
 }
 
 template cudaError_t prepare_recon<ShapeMain>();

@@ -1,0 +1,81 @@
+// Device side of rcp_score_mod: which cached tokens a query row sees, and what happens to its
+// scores before the softmax.  Shared by the decode and prefill kernels.
+#pragma once
+#include <cstdint>
+
+#include "shape.h"
+
+namespace rcp {
+
+// What a row at position pos of a request with L tokens sees: tokens t < pfx, and tokens
+// lo <= t <= pos (lo >= pos + 1: none of those).
+struct RowView {
+  int32_t pfx, lo;
+};
+
+__device__ __forceinline__ int32_t view_prefix(const AttnParams& p, int b, int32_t L) {
+  const int32_t f = p.prefix_lens ? p.prefix_lens[b] : 0;
+  return f < 0 ? 0 : (f < L ? f : L);
+}
+// First token behind the prefix that row `row` (of the call's query rows), at position pos,
+// may see: the later of its row_begin and its window's start.
+__device__ __forceinline__ int32_t view_begin(const AttnParams& p, int64_t row, int32_t pos) {
+  int32_t lo = p.row_begin ? p.row_begin[row] : 0;
+  if (p.window > 0 && pos + 1 - p.window > lo) lo = pos + 1 - p.window;
+  return lo > 0 ? lo : 0;
+}
+
+// The position a row's distance bias is measured from: its own when it sees itself, else the
+// last token of the prefix.  The softmax does not change when a constant is added to a row's
+// scores, so only differences of distances count; measured from the nearest visible token
+// the bias of the tokens that carry weight stays small, and fp32 exact to its last bits.
+__device__ __forceinline__ int32_t bias_origin(RowView v, int32_t pos) {
+  return (v.lo <= pos || pos < v.pfx) ? pos : v.pfx - 1;
+}
+
+// cap2 tanh(x / cap2), x and cap2 in log2 units
+__device__ __forceinline__ float cap_score(float x, float cap2, float inv_cap2) {
+  return cap2 * tanhf(x * inv_cap2);
+}
+
+// A prefill request's key tiles (KT keys) that some of its rows sees: those of the prefix and
+// those from the least first token of any row on, from the plan's (prefix, least first token).
+// Their pages, one after another, are the rows of V^ (reconstructing variant) and the pages
+// the widening pass copies; key tile x is number compact(x) among them.
+template <class S>
+struct TileMap {
+  static constexpr int KT = PrefillCfg<S>::KT, BPT = KT / kBlockSize;
+  int32_t pfx, lo, np, lt, nblk;   // np prefix tiles, then tiles lt .. ; pages of the request
+  __device__ __forceinline__ TileMap(const int32_t* m, int32_t nb) : pfx(m[0]), lo(m[1]), nblk(nb) {
+    const int32_t tiles = (nblk + BPT - 1) / BPT;
+    np = (pfx + KT - 1) / KT;
+    lt = lo / KT;
+    if (lo >= nblk * kBlockSize || lt > tiles) lt = tiles;
+    if (lt < np) lt = np;
+  }
+  __device__ __forceinline__ int32_t pages() const {
+    const int32_t a = np * BPT < nblk ? np * BPT : nblk, b = nblk - lt * BPT;
+    return a + (b > 0 ? b : 0);
+  }
+  __device__ __forceinline__ int32_t compact(int32_t tile) const {
+    return tile < np ? tile : np + (tile - lt);
+  }
+  // page of the request that is number j of them
+  __device__ __forceinline__ int32_t page(int32_t j) const {
+    return j < np * BPT ? j : (lt - np) * BPT + j;
+  }
+  // whether some row may see a token of page x (another one's table entry is not looked at)
+  __device__ __forceinline__ bool seen(int32_t x) const {
+    return x * kBlockSize < pfx || (x + 1) * kBlockSize > lo;
+  }
+};
+
+// Bits c of a 32-column word starting at column c0 whose columns lie in [a, b).
+__device__ __forceinline__ uint32_t column_bits(int32_t a, int32_t b, int32_t c0) {
+  const int32_t lo = a - c0, hi = b - c0;
+  const uint32_t up = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t dn = lo >= 32 ? 0xFFFFFFFFu : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return up & ~dn;
+}
+
+}  // namespace rcp

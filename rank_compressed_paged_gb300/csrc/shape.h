@@ -132,7 +132,7 @@ inline WsLayout ws_layout(int64_t nq) {
 // its per-request block prefix sums and the reconstructed values V^ start where they
 // start, for at most batch x max_blocks_per_seq pages.
 struct ReconLayout {
-  size_t vcum, vhat, kw, vw, tw, total;
+  size_t vcum, vmap, vhat, kw, vw, tw, total;
 };
 // widen (E4M3 pages): also fp16 copies of the pages the batch reads, [pages][H][16][r_k]
 // and [pages][16][R], and the block table re-addressed to them, [batch][max_blocks].
@@ -143,6 +143,7 @@ inline ReconLayout recon_layout(int64_t nq, int64_t batch, int64_t max_blocks, b
   ReconLayout r;
   size_t o = w.rec;
   r.vcum = o;  o = align256(o + sizeof(int64_t) * (batch + 1));
+  r.vmap = o;  o = align256(o + 2 * sizeof(int32_t) * batch);
   r.vhat = o;  o = align256(o + 2 * pages * kBlockSize * S::H * S::D);
   r.kw = r.vw = r.tw = 0;
   if (widen) {
@@ -199,6 +200,15 @@ struct AttnParams {
   const int64_t* slots;
   int32_t n_slots;
   float qscale;               // log2(e) / sqrt(d)
+  // score modifications (rcp_score_mod): set when mod != 0
+  int32_t mod;
+  int32_t window;             // > 0: tokens t > pos - window
+  float cap2;                 // score cap in log2 units (0: none), and its reciprocal
+  float inv_cap2;
+  const float* slopes;        // [H] distance bias per token, or nullptr
+  const int32_t* prefix_lens; // [batch] tokens every row of the request sees, or nullptr
+  const int32_t* row_begin;   // [nq] first token a row sees behind the prefix, or nullptr
+  int32_t* vmap;              // prefill plan: [batch][2] (prefix, least first token of any row)
 };
 
 // What the split-K combine + up-projection of a decode call sees (combine.cu).
@@ -212,6 +222,31 @@ struct CombineParams {
   uint32_t* dev_err;
   int32_t nq;
   int32_t parts;              // split-K partitions launched
+};
+
+// Page copies (pages.cu): pair i copies pages pairs[2 i] to pairs[2 i + 1].
+struct CopyParams {
+  void* k_pages;
+  void* v_pages;
+  const int32_t* pairs;       // [n][2] device, or nullptr: one source, the listed ids
+  uint32_t* dev_err;
+  int64_t num_blocks;
+  int32_t n;
+  int32_t src;                // pairs == nullptr
+};
+
+// In-place compaction (pages.cu).
+struct CompactParams {
+  void* k_pages;
+  void* v_pages;
+  const int32_t* block_table; // [batch][bt_stride]
+  const int32_t* seq_lens;    // [batch]
+  const uint8_t* keep;        // [batch][bt_stride * 16]
+  int32_t* new_lens;          // [batch]
+  uint32_t* dev_err;
+  int64_t num_blocks;
+  int32_t bt_stride;
+  int32_t batch;
 };
 
 struct AppendParams {

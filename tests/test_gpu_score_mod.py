@@ -1,0 +1,442 @@
+"""Score-modified decode and chunked prefill vs the fp64 oracle, through the C ABI (needs a
+GB300): capped scores, distance bias, windows, prefixes and document masks on every page
+format and both shapes."""
+import numpy as np
+import pytest
+
+import workloads as wl
+from oracle import rcp_oracle as orc
+from tests.mod_util import assert_within, cache_of, encode, score_mod, values
+from tests.gpu_util import t
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = {"tiny": wl.SHAPES["tiny"], "main": wl.SHAPES["mha32"]}
+FORMATS = ["fp16", "fp8_e4m3", "int4"]
+LENS = [0, 1, 15, 16, 17, 33, 200, 256, 385, 500]
+
+
+def slopes_of(shape):
+    H = shape["num_heads"]
+    return [2.0 ** (-8 * (h + 1) / H) for h in range(H)]
+
+
+def decode_mods(shape, lens):
+    L = np.asarray(lens)
+    return {
+        "cap": dict(softcap=5.0),
+        "bias": dict(alibi_slopes=slopes_of(shape)),
+        "window": dict(window=23),
+        "window1": dict(window=1),
+        "sinks": dict(window=40, prefix_lens=np.minimum(L, 5)),
+        "prefix": dict(prefix_lens=np.full(len(L), 35), row_begin=L),     # the prefix alone
+        "hole": dict(prefix_lens=np.full(len(L), 3), row_begin=np.full(len(L), 9)),
+        "docs": dict(row_begin=L * 2 // 3, softcap=20.0),
+        "empty": dict(row_begin=L + 1),
+        "odd": dict(prefix_lens=np.array([-4, 2 ** 31 - 1] * (len(L) // 2)),
+                    row_begin=np.array([2 ** 31 - 1, -7] * (len(L) // 2))),
+        "all": dict(softcap=3.0, alibi_slopes=slopes_of(shape), window=100,
+                    prefix_lens=np.full(len(L), 18), row_begin=L // 2),
+    }
+
+
+_decode_cache = {}
+
+
+def decode_inputs(shape_name, pages, lens=LENS, seed=301, scale=4.0):
+    key = (shape_name, pages, tuple(lens), seed)
+    if key not in _decode_cache:
+        shape = SHAPES[shape_name]
+        inp = wl.make_decode_inputs(shape, lens, seed=seed, fill=np.nan if pages == "fp16" else 0.0)
+        inp.q = wl.fp16(inp.q.astype(np.float64) * scale)
+        inp.k, inp.v = encode(pages, inp.cache.k_pages, inp.cache.v_pages)
+        _decode_cache[key] = inp
+    return _decode_cache[key]
+
+
+def oracle_decode(inp, pages, mod, k=None, v=None):
+    kk, vv = values(pages, inp.shape, inp.k if k is None else k, inp.v if v is None else v, False)
+    ref = orc.decode_attn_mod(inp.q, kk, vv, inp.U_k, inp.W_v, inp.cache.block_table,
+                              inp.cache.seq_lens, magnitudes=True, **mod)
+    return (*ref, int(max(inp.cache.seq_lens)))
+
+
+@pytest.mark.parametrize("name", sorted(decode_mods(SHAPES["tiny"], LENS)))
+@pytest.mark.parametrize("pages", FORMATS)
+@pytest.mark.parametrize("shape_name", ["tiny", "main"])
+def test_decode_matches_oracle(shape_name, pages, name):
+    import torch
+    inp = decode_inputs(shape_name, pages)
+    mod = decode_mods(inp.shape, LENS)[name]
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+    out = cache.decode_attn(t(inp.q), t(inp.cache.block_table), t(inp.cache.seq_lens),
+                            mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert_within(out.cpu().numpy(), oracle_decode(inp, pages, mod), f"{shape_name} {pages} {name}")
+
+
+@pytest.mark.parametrize("pages", FORMATS)
+@pytest.mark.parametrize("shape_name", ["tiny", "main"])
+def test_decode_without_effective_modifications_is_the_plain_decode(shape_name, pages):
+    """Masks that hide nothing and a zero bias leave every operation as it was."""
+    inp = decode_inputs(shape_name, pages)
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+    args = t(inp.q), t(inp.cache.block_table), t(inp.cache.seq_lens)
+    plain = cache.decode_attn(*args).cpu().numpy().view(np.uint16)
+    B, H = len(LENS), inp.shape["num_heads"]
+    for mod in (dict(), dict(window=500), dict(row_begin=np.zeros(B)),
+                dict(alibi_slopes=np.zeros(H)), dict(prefix_lens=np.full(B, 600))):
+        got = cache.decode_attn(*args, mod=score_mod(mod)).cpu().numpy().view(np.uint16)
+        assert np.array_equal(plain, got), mod
+
+
+@pytest.mark.parametrize("pages", FORMATS)
+@pytest.mark.parametrize("mod", [dict(window=4100, prefix_lens=[70]),
+                                 dict(row_begin=[3000], softcap=30.0),
+                                 dict(softcap=50.0)])
+def test_decode_of_one_long_request(pages, mod):
+    """One request over many partitions: partial records of the visible pages only."""
+    import torch
+    inp = decode_inputs("main", pages, lens=[7003], seed=302)
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+    out = cache.decode_attn(t(inp.q), t(inp.cache.block_table), t(inp.cache.seq_lens),
+                            mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert_within(out.cpu().numpy(), oracle_decode(inp, pages, mod), f"long {pages} {mod}")
+
+
+def hide(inp, pages, k, v, b, tokens):
+    """Fills the slots of tokens with the worst bytes the format has: NaN (fp16, E4M3), NaN
+    scales and codes of -8 (4-bit)."""
+    H, rk, R = (inp.shape[x] for x in ("num_heads", "rank_k", "rank_v"))
+    for tok in tokens:
+        blk, off = inp.cache.block_table[b, tok // 16], tok % 16
+        if pages == "int4":
+            kc, vc = H * 16 * rk // 2, 16 * R // 2
+            for h in range(H):
+                row = h * 16 + off
+                k[blk, row * rk // 2:(row + 1) * rk // 2] = 0x88
+                k[blk, kc + 2 * row:kc + 2 * row + 2] = (0x00, 0x7E)
+            v[blk, off * R // 2:(off + 1) * R // 2] = 0x88
+            n = R // 64 * 2
+            v[blk, vc + off * n:vc + (off + 1) * n] = np.tile(np.uint8([0x00, 0x7E]), R // 64)
+        else:
+            k[blk, :, off] = np.nan if pages == "fp16" else 0x7F
+            v[blk, off] = np.nan if pages == "fp16" else 0x7F
+
+
+@pytest.mark.parametrize("pages", FORMATS)
+@pytest.mark.parametrize("shape_name", ["tiny", "main"])
+def test_decode_hidden_tokens_may_hold_anything_and_their_pages_may_be_gone(shape_name, pages):
+    import torch
+    lens = [300, 301, 90]
+    inp = decode_inputs(shape_name, pages, lens=lens, seed=303)
+    mod = dict(window=50, prefix_lens=[21, 0, 21], row_begin=[0, 280, 60], softcap=9.0)
+    seen = [orc.visible_tokens(L - 1, L, mod["prefix_lens"][b], mod["row_begin"][b], 50)
+            for b, L in enumerate(lens)]
+    k, v = inp.k.copy(), inp.v.copy()
+    table = inp.cache.block_table.copy()
+    for b, L in enumerate(lens):
+        hide(inp, pages, k, v, b, np.nonzero(~seen[b])[0])
+        for j in range((L + 15) // 16):
+            if not seen[b][16 * j:16 * j + 16].any():
+                table[b, j] = (-5, 1 << 30)[j % 2]         # freed: the entry is not looked at
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, k, v)
+    out = cache.decode_attn(t(inp.q), t(table), t(inp.cache.seq_lens), mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert_within(out.cpu().numpy(), oracle_decode(inp, pages, mod), f"hidden {pages}")
+
+
+def test_decode_bad_block_among_the_visible_pages_is_reported_and_left_out():
+    import torch
+    from rank_compressed_paged_gb300 import _lib
+    inp = decode_inputs("main", "fp16", lens=[200, 200], seed=304)
+    mod = dict(window=100, softcap=9.0)
+    table = inp.cache.block_table.copy()
+    table[1, 9] = inp.k.shape[0] + 3
+    cache = cache_of("fp16", inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+    out = cache.decode_attn(t(inp.q), t(table), t(inp.cache.seq_lens), mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == _lib.RCP_DEVERR_BAD_BLOCK
+    see = orc.visible_tokens(199, 200, window=100)
+    see[144:160] = False
+    ck, cv = orc.gather_request(inp.k, inp.v, inp.cache.block_table[1], 200, 16)
+    want, _ = orc.attend_mod(inp.q[1:2], ck, cv, inp.U_k, inp.W_v, 128, [199], see[None], 9.0)
+    ref = oracle_decode(inp, "fp16", mod)
+    got = out.cpu().numpy()
+    assert_within(got[:1], (ref[0][:1], ref[1][:1], ref[2][:1], 200), "unaffected request")
+    np.testing.assert_allclose(got[1], want[0], rtol=0, atol=2e-3)
+
+
+def test_decode_bad_lengths_give_zeros():
+    import torch
+    from rank_compressed_paged_gb300 import _lib
+    inp = decode_inputs("tiny", "fp16", lens=[40, 40, 40], seed=305)
+    cache = cache_of("fp16", inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+    lens = np.array([-3, 40, 49], np.int32)          # 3 table columns: 48 tokens
+    out = cache.decode_attn(t(inp.q), t(inp.cache.block_table), t(lens),
+                            mod=score_mod(dict(window=7, prefix_lens=[9, 9, 9])))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == _lib.RCP_DEVERR_BAD_LEN
+    o = out.cpu().numpy()
+    assert np.all(o[0] == 0) and np.all(o[2] == 0) and np.any(o[1] != 0)
+
+
+@pytest.mark.parametrize("pages", FORMATS)
+def test_decode_step_appends_first(pages):
+    """The step's own token is the newest visible one; in a graph, with the masks rewritten
+    between replays."""
+    import torch
+    lens = [100, 17, 16, 1]
+    shape = SHAPES["main"]
+    inp = wl.make_decode_inputs(shape, lens, seed=306, append=True)
+    k0, v0 = encode(pages, inp.cache.k_pages, inp.cache.v_pages)
+    cache = cache_of(pages, shape, inp.U_k, inp.W_v, k0, v0)
+    mods = [dict(softcap=7.0, window=20, row_begin=[0, 0, 3, 0], prefix_lens=[4, 0, 0, 1]),
+            dict(softcap=7.0, window=20, row_begin=[90, 17, 0, 0], prefix_lens=[0, 2, 5, 0])]
+    dev = score_mod(mods[0])
+    k, v, sl, q = t(inp.new_k), t(inp.new_v), t(inp.slot_mapping), t(inp.q)
+    table, sq = t(inp.cache.block_table), t(inp.cache.seq_lens)
+    ws = cache.workspace(len(lens))
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.decode_step(k, v, sl, q, table, sq, out=out, workspace=ws, mod=dev)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.decode_step(k, v, sl, q, table, sq, out=out, workspace=ws, mod=dev)
+    for mod in mods:
+        dev.row_begin.copy_(t(np.asarray(mod["row_begin"], np.int32)))
+        dev.prefix_lens.copy_(t(np.asarray(mod["prefix_lens"], np.int32)))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert cache.read_device_error() == 0
+        kk, vv = values(pages, shape, cache.k_pages.cpu().numpy(), cache.v_pages.cpu().numpy(), False)
+        ref = orc.decode_attn_mod(inp.q, kk, vv, inp.U_k, inp.W_v, inp.cache.block_table,
+                                  inp.cache.seq_lens, magnitudes=True, **mod)
+        assert_within(out.cpu().numpy(), (*ref, 100), f"step {pages}")
+    # the append wrote the same pages as the plain step's
+    other = cache_of(pages, shape, inp.U_k, inp.W_v, k0, v0)
+    other.append_kv(k, v, sl)
+    assert torch.equal(cache.k_pages.view(torch.uint8), other.k_pages.view(torch.uint8))
+    assert torch.equal(cache.v_pages.view(torch.uint8), other.v_pages.view(torch.uint8))
+
+
+# ------------------------------------------------------------------------------- prefill
+PRIOR, CHUNK = [0, 37, 300, 5, 130, 17], [40, 21, 150, 0, 1, 290]
+
+
+def doc_begin(rows, prior, chunk, size):
+    """Start of the document (every ``size`` tokens) that each chunk row belongs to."""
+    return np.concatenate([(p + np.arange(c)) // size * size for p, c in zip(prior, chunk)])
+
+
+def prefill_mods(shape):
+    rows = sum(CHUNK)
+    B = len(PRIOR)
+    rng = np.random.default_rng(1)
+    pos = np.concatenate([p + np.arange(c) for p, c in zip(PRIOR, CHUNK)])
+    pad = np.where(rng.random(rows) < 0.3, 2 ** 31 - 1, 0)
+    return {
+        "cap": dict(softcap=5.0),
+        "bias": dict(alibi_slopes=slopes_of(shape)),
+        "window": dict(window=60),
+        "window1": dict(window=1),
+        "sinks": dict(window=33, prefix_lens=np.full(B, 4)),
+        "prefix_lm": dict(prefix_lens=np.array([25, 50, 400, 0, 2 ** 31 - 1, 150])),
+        "prefix_bias": dict(prefix_lens=np.full(B, 140), alibi_slopes=slopes_of(shape), window=3),
+        "prefix_only": dict(prefix_lens=np.full(B, 10), row_begin=pos + 1,
+                            alibi_slopes=slopes_of(shape)),
+        "docs": dict(row_begin=doc_begin(rows, PRIOR, CHUNK, 29)),
+        "docs_long": dict(row_begin=doc_begin(rows, PRIOR, CHUNK, 171), softcap=20.0),
+        "empty_rows": dict(row_begin=pad),
+        "empty": dict(row_begin=pos + 1),
+        "self_only": dict(row_begin=pos),
+        "all": dict(softcap=3.0, alibi_slopes=slopes_of(shape), window=100,
+                    prefix_lens=np.full(B, 18), row_begin=doc_begin(rows, PRIOR, CHUNK, 171)),
+    }
+
+
+_prefill_cache = {}
+
+
+def prefill_inputs(shape_name, pages):
+    key = (shape_name, pages)
+    if key not in _prefill_cache:
+        shape = SHAPES[shape_name]
+        inp = wl.make_prefill_inputs(shape, PRIOR, CHUNK, seed=311,
+                                     fill=np.nan if pages == "fp16" else 0.0)
+        inp.q = wl.fp16(inp.q.astype(np.float64) * 4)
+        # every token's coefficients as given (the append has tests of its own)
+        rng = np.random.default_rng(312)
+        c = inp.cache
+        kp, vp = c.k_pages.copy(), c.v_pages.copy()
+        for b, L in enumerate(inp.seq_lens_after):
+            for j in range((int(L) + 15) // 16):
+                n = min(16, int(L) - 16 * j)
+                blk = c.block_table[b, j]
+                kp[blk, :, :n] = wl.fp16(rng.standard_normal(kp[blk, :, :n].shape))
+                vp[blk, :n] = wl.fp16(rng.standard_normal(vp[blk, :n].shape))
+        inp.kp, inp.vp = encode(pages, kp, vp)
+        _prefill_cache[key] = inp
+    return _prefill_cache[key]
+
+
+_ref_cache = {}
+
+
+def oracle_prefill(inp, shape_name, pages, name, mod):
+    key = (shape_name, pages, name)
+    if key not in _ref_cache:
+        kk, vv = values(pages, inp.shape, inp.kp, inp.vp, True)
+        ref = orc.prefill_attn_mod(inp.q, inp.cu_chunk_lens, kk, vv, inp.U_k, inp.W_v,
+                                   inp.cache.block_table, inp.seq_lens_after, magnitudes=True, **mod)
+        _ref_cache[key] = (*ref, int(max(inp.seq_lens_after)))
+    return _ref_cache[key]
+
+
+CASES = [("main", "fp16", m) for m in sorted(prefill_mods(SHAPES["main"]))] + \
+        [("tiny", p, m) for p in FORMATS for m in sorted(prefill_mods(SHAPES["tiny"]))] + \
+        [("main", p, m) for p in ("fp8_e4m3", "int4") for m in ("all", "docs", "prefix_bias")]
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("shape_name,pages,name", CASES)
+def test_prefill_matches_oracle(shape_name, pages, name, variant):
+    import torch
+    inp = prefill_inputs(shape_name, pages)
+    mod = prefill_mods(inp.shape)[name]
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    out = torch.full(inp.q.shape, float("nan"), dtype=torch.float16, device="cuda")
+    cache.prefill_attn(t(inp.q), t(inp.cu_chunk_lens), t(inp.cache.block_table),
+                       t(inp.seq_lens_after), out=out, variant=variant, mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert_within(out.cpu().numpy(), oracle_prefill(inp, shape_name, pages, name, mod),
+                  f"{shape_name} {pages} {name} {variant}")
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("tiny", "fp8_e4m3"), ("tiny", "int4")])
+def test_prefill_without_effective_modifications_is_the_plain_prefill(shape_name, pages, variant):
+    inp = prefill_inputs(shape_name, pages)
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    args = (t(inp.q), t(inp.cu_chunk_lens), t(inp.cache.block_table), t(inp.seq_lens_after))
+    plain = cache.prefill_attn(*args, variant=variant).cpu().numpy().view(np.uint16)
+    rows, H = sum(CHUNK), inp.shape["num_heads"]
+    for mod in (dict(), dict(window=1000), dict(row_begin=np.zeros(rows)),
+                dict(alibi_slopes=np.zeros(H)), dict(prefix_lens=np.zeros(len(PRIOR)))):
+        got = cache.prefill_attn(*args, variant=variant, mod=score_mod(mod))
+        assert np.array_equal(plain, got.cpu().numpy().view(np.uint16)), mod
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("main", "fp8_e4m3"),
+                                              ("tiny", "fp16"), ("tiny", "int4")])
+def test_prefill_hidden_tokens_may_hold_anything_and_their_pages_may_be_gone(shape_name, pages,
+                                                                             variant):
+    """Tokens no row sees (before every window, and padding rows in the middle of the chunk)
+    hold NaN; pages before every row's first token and behind the prefix are gone."""
+    import torch
+    inp = prefill_inputs(shape_name, pages)
+    B, rows = len(PRIOR), sum(CHUNK)
+    begin = np.zeros(rows, np.int64)
+    at = 0
+    for p, c in zip(PRIOR, CHUNK):          # document, padding, document
+        for i in range(c):
+            if c // 3 <= i < c // 2:
+                begin[at + i] = 2 ** 31 - 1
+            elif i >= c // 2:
+                begin[at + i] = p + c // 2
+        at += c
+    mod = dict(window=45, prefix_lens=np.full(B, 19), row_begin=begin, softcap=9.0)
+    k, v = inp.kp.copy(), inp.vp.copy()
+    table = inp.cache.block_table.copy()
+    hidden = 0
+    for b in range(B):
+        L, c0, c1 = int(inp.seq_lens_after[b]), inp.cu_chunk_lens[b], inp.cu_chunk_lens[b + 1]
+        if c1 == c0:
+            continue
+        see = np.stack([orc.visible_tokens(L - (c1 - c0) + i, L, 19, begin[c0 + i], 45)
+                        for i in range(c1 - c0)]).any(axis=0)
+        hide(inp, pages, k, v, b, np.nonzero(~see)[0])
+        hidden += int((~see).sum())
+        first = np.nonzero(see[19:])[0][0] + 19 if see[19:].any() else L
+        for j in range(2, first // 16):
+            table[b, j] = (-5, 1 << 30)[j % 2]
+    assert hidden > 100
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, k, v)
+    out = cache.prefill_attn(t(inp.q), t(inp.cu_chunk_lens), t(table), t(inp.seq_lens_after),
+                             variant=variant, mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert_within(out.cpu().numpy(), oracle_prefill(inp, shape_name, pages, "hidden", mod),
+                  f"hidden {shape_name} {pages} {variant}")
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+def test_prefill_bad_block_is_reported_and_left_out(variant):
+    import torch
+    from rank_compressed_paged_gb300 import _lib
+    inp = prefill_inputs("main", "fp16")
+    mod = dict(window=200, softcap=9.0)
+    table = inp.cache.block_table.copy()
+    table[2, 20] = -1                                    # request 2: tokens 320 .. 335
+    cache = cache_of("fp16", inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    out = cache.prefill_attn(t(inp.q), t(inp.cu_chunk_lens), t(table), t(inp.seq_lens_after),
+                             variant=variant, mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == _lib.RCP_DEVERR_BAD_BLOCK
+    got = out.cpu().numpy()
+    ref = oracle_prefill(inp, "main", "fp16", "bad", mod)
+    c0, c1 = inp.cu_chunk_lens[2], inp.cu_chunk_lens[3]
+    rest = np.r_[0:c0, c1:sum(CHUNK)]
+    assert_within(got[rest], (ref[0][rest], ref[1][rest], ref[2][rest], ref[3]), "other requests")
+    L, n = 450, 150
+    see = np.stack([orc.visible_tokens(300 + i, L, window=200) for i in range(n)])
+    see[:, 320:336] = False
+    ck, cv = orc.gather_request(inp.kp, inp.vp, inp.cache.block_table[2], L, 16)
+    want, _ = orc.attend_mod(inp.q[c0:c1], ck, cv, inp.U_k, inp.W_v, 128, 300 + np.arange(n), see, 9.0)
+    np.testing.assert_allclose(got[c0:c1], want, rtol=0, atol=4e-3)
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+def test_prefill_step_appends_first_and_replays_on_a_side_stream(variant):
+    import torch
+    shape = SHAPES["main"]
+    inp = wl.make_prefill_inputs(shape, [100, 3], [140, 20], seed=313)
+    c = inp.cache
+    cache = cache_of("fp16", shape, inp.U_k, inp.W_v, c.k_pages, c.v_pages)
+    mod = dict(window=130, prefix_lens=[10, 23], softcap=6.0, alibi_slopes=slopes_of(shape))
+    dev = score_mod(mod)
+    args = (t(inp.k), t(inp.v), t(inp.slot_mapping), t(inp.q), t(inp.cu_chunk_lens),
+            t(c.block_table), t(inp.seq_lens_after))
+    ws = torch.empty(cache.reconstruct_workspace_bytes(160, 2, c.block_table.shape[1]),
+                     dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(args[3])
+    kp, vp = orc.append_kv(c.k_pages, c.v_pages, inp.U_k, inp.W_v, inp.k, inp.v, inp.slot_mapping)
+    ref = (*orc.prefill_attn_mod(inp.q, inp.cu_chunk_lens, kp, vp, inp.U_k, inp.W_v, c.block_table,
+                                 inp.seq_lens_after, magnitudes=True, **mod), 240)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.prefill_step(*args, out=out, workspace=ws, variant=variant, mod=dev)
+    side.synchronize()
+    # one fp16 ulp of an appended coefficient moves a value by 2^-11 of it and a score likewise
+    np.testing.assert_allclose(out.cpu().numpy(), ref[0], rtol=0, atol=4e-3)
+    eager = out.clone()
+    out.fill_(float("nan"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        cache.prefill_step(*args, out=out, workspace=ws, variant=variant, mod=dev)
+    g.replay()
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert torch.equal(eager, out)
