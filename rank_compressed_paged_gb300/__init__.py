@@ -28,6 +28,15 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+def _fits(shape, want) -> bool:
+    if len(shape) != len(want):
+        return False
+    for have, e in zip(shape, want):
+        if e is not None and have != e:
+            return False
+    return True
+
+
 def _need(name: str, x, dtype, shape=None, device=None) -> None:
     """Check one tensor argument before its pointer crosses the C ABI, which cannot see
     dtypes, strides or devices: raise ValueError unless ``x`` is a contiguous tensor of
@@ -37,11 +46,9 @@ def _need(name: str, x, dtype, shape=None, device=None) -> None:
         raise ValueError(f"{name} must be a torch.Tensor, got {type(x).__name__}")
     if x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if shape is not None:
-        if x.dim() != len(shape) or any(e is not None and x.shape[i] != e
-                                        for i, e in enumerate(shape)):
-            want = "[" + ", ".join("*" if e is None else str(e) for e in shape) + "]"
-            raise ValueError(f"{name} must have shape {want}, got {list(x.shape)}")
+    if shape is not None and not _fits(x.shape, shape):
+        want = "[" + ", ".join("*" if e is None else str(e) for e in shape) + "]"
+        raise ValueError(f"{name} must have shape {want}, got {list(x.shape)}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if device is not None and x.device != device:

@@ -140,6 +140,7 @@ cudaError_t prepare_kernels(int dev) {
   if (e == cudaSuccess) e = rcp::prepare_combine<S>();
   if (e == cudaSuccess) e = rcp::prepare_prefill<S>();
   if (e == cudaSuccess) e = rcp::prepare_recon<S>();
+  if (e == cudaSuccess) e = rcp::prepare_pages<S>();
   return e;
 }
 
@@ -765,8 +766,8 @@ rcp_status rcp_compact_tokens(rcp_cache* c, const int32_t* block_table, int32_t 
   p.batch = batch;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = c->shape == kShapeMain
-                            ? rcp::launch_compact<ShapeMain>(p, c->cfg.page_format, s)
-                            : rcp::launch_compact<ShapeTiny>(p, c->cfg.page_format, s);
+                            ? rcp::launch_compact<ShapeMain>(p, c->cfg.page_format, c->num_sms, s)
+                            : rcp::launch_compact<ShapeTiny>(p, c->cfg.page_format, c->num_sms, s);
   return e == cudaSuccess ? RCP_OK : RCP_ERR_CUDA;
 }
 

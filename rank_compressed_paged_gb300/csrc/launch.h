@@ -68,8 +68,11 @@ constexpr int kCopyListMax = 960;   // the kernel's parameters stay below 4 KiB
 template <class S>
 cudaError_t launch_copy_pages(const CopyParams& p, const int32_t* list, int page_format,
                               int num_sms, cudaStream_t stream);
+template <class S>
+cudaError_t prepare_pages();
 // In-place compaction of every request's kept tokens (pages.cu).
 template <class S>
-cudaError_t launch_compact(const CompactParams& p, int page_format, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, int page_format, int num_sms,
+                           cudaStream_t stream);
 
 }  // namespace rcp

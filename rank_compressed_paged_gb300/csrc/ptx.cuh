@@ -356,6 +356,10 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// The same meeting point without ordering any memory access.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Shared-memory address of the same variable in the CTA of cluster rank `rank`.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t local_smem, uint32_t rank) {
   uint32_t r;

@@ -247,6 +247,7 @@ struct CompactParams {
   int64_t num_blocks;
   int32_t bt_stride;
   int32_t batch;
+  int32_t ctas;               // CTAs (a cluster) per slice of a request
 };
 
 struct AppendParams {
