@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     // MOD: what this row sees, its head's bias per token (log2 units) and where it starts from
     RowView view{pfx, 0};
+    bool far = false;          // a score passed the range of the cap's polynomial
     int32_t org = 0;
     float slope2 = 0.f;
     if constexpr (MOD) {
@@ -430,15 +431,48 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key
       uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
+      float shift = 0.f;                                // MOD: to be added to every score
       if constexpr (MOD) {
         if (ok && p.cap2 > 0.f) {
+          if (!far) {
+            float vmax = 0.f;
 #pragma unroll
-          for (int c = 0; c < KT; ++c) sv[c] = cap_score(sv[c], p.cap2, p.inv_cap2);
+            for (int c = 0; c < KT; c += 2) {
+              const float2 y = cap_pair_near(make_float2(sv[c], sv[c + 1]), p.inv_cap2, vmax);
+              sv[c] = y.x;
+              sv[c + 1] = y.y;
+            }
+            if (__any_sync(0xffffffffu, !(vmax <= kCapNear))) {
+              // some score is past the polynomial's range (or NaN): the tile's scores are
+              // still in tensor memory; the warp stays with the general form from here on
+              far = true;
+#pragma unroll
+              for (int c = 0; c < KT; c += 16)
+                tmem_ld16(tl + s * 128 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+              tmem_wait_ld();
+            }
+          }
+          if (far) {
+#pragma unroll
+            for (int c = 0; c < KT; c += 2) {
+              const float2 y = cap_pair_far(make_float2(sv[c], sv[c + 1]), p.cap2, p.inv_cap2);
+              sv[c] = y.x;
+              sv[c + 1] = y.y;
+            }
+          }
         }
         if (ok && p.slopes) {
-          const float d0 = static_cast<float>(org - t0);
+          if (__all_sync(0xffffffffu, t0 + KT - 1 <= org)) {
+            // every key at or before the origin: slope (t - org), its tile-wide part kept apart
+            shift = slope2 * static_cast<float>(t0 - org);
 #pragma unroll
-          for (int c = 0; c < KT; ++c) sv[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
+            for (int c = 0; c < KT; ++c) sv[c] = fmaf(slope2, static_cast<float>(c), sv[c]);
+          } else {
+            const float d0 = static_cast<float>(org - t0);
+#pragma unroll
+            for (int c = 0; c < KT; ++c)
+              sv[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
+          }
         }
         // a tile that every row of the CTA sees whole needs no mask
         const uint32_t bad = static_cast<uint32_t>(sbad[s]);
@@ -491,13 +525,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           m4[3] = max3f(m4[3], sv[c + 6], sv[c + 7]);
         }
         mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+        if constexpr (MOD) mx += shift;
       }
       const float m_new = (mx > m_run + kPfRescale) ? mx : m_run;
       const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
       uint32_t packed[KT / 2];
       float rsum;
       {
-        const float msub = (m_new == -INFINITY) ? 0.f : m_new;   // rows with no valid key
+        // rows with no valid key
+        const float msub = (m_new == -INFINITY) ? 0.f : (MOD ? m_new - shift : m_new);
         const float2 msub2 = make_float2(msub, msub);
         float2 s4[4];
 #pragma unroll

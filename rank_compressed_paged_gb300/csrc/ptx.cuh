@@ -388,6 +388,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // Named barrier over a subset of warps (id 1..15).
+__device__ __forceinline__ float fast_rcp(float x) {   // relative error about 2^-23; inf gives 0
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Three-input maximum (one instruction on sm_100 and later).
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
@@ -408,6 +413,13 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
       : "=l"(d)
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
         "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
   return *reinterpret_cast<const float2*>(&d);
 }
 __device__ __forceinline__ float2 sub_f32x2(float2 a, float2 b) {

@@ -70,6 +70,36 @@ struct TileMap {
   }
 };
 
+// cap2 tanh(x / cap2) of a pair of scores, log2 units, for the prefill, where a row meets 128
+// of them per tile.  Scores well below the cap (|x| <= 0.7 cap2) take a polynomial: with
+// u = x / cap2 and v = u^2, tanh(u) / u = 1 + v q(v), q the least-maximum fit of degree 3 on
+// v in [0, 0.49] (relative error 3.2e-7).  vmax collects the largest v; the caller goes to
+// cap_pair_far if it passed kCapNear.
+constexpr float kCapNear = 0.49f;
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 cap_pair_near(float2 x, float inv_cap2, float& vmax) {
+  const float2 u = mul_f32x2(x, both(inv_cap2)), v = mul_f32x2(u, u);
+  float2 q = fma_f32x2(both(0.013981962f), v, both(-0.0510577062f));
+  q = fma_f32x2(q, v, both(0.132888389f));
+  q = fma_f32x2(q, v, both(-0.333311808f));
+  vmax = max3f(vmax, v.x, v.y);
+  return fma_f32x2(mul_f32x2(x, v), q, x);
+}
+// Any score: 1 - 2 / (e^2u + 1) past the polynomial's range (absolute error about 3e-7 of the
+// cap, below 7e-7 of the result there), the polynomial within it.
+__device__ __forceinline__ float cap_far(float x, float cap2, float inv_cap2) {
+  const float e = fast_exp2(x * inv_cap2 * 2.88539008f);
+  return fmaf(-2.f * cap2, fast_rcp(e + 1.f), cap2);
+}
+__device__ __forceinline__ float2 cap_pair_far(float2 x, float cap2, float inv_cap2) {
+  float vx = 0.f, vy = 0.f;
+  const float2 n = cap_pair_near(x, inv_cap2, vx);
+  vx = x.x * inv_cap2;
+  vy = x.y * inv_cap2;
+  return make_float2(vx * vx <= kCapNear ? n.x : cap_far(x.x, cap2, inv_cap2),
+                     vy * vy <= kCapNear ? n.y : cap_far(x.y, cap2, inv_cap2));
+}
+
 // Bits c of a 32-column word starting at column c0 whose columns lie in [a, b).
 __device__ __forceinline__ uint32_t column_bits(int32_t a, int32_t b, int32_t c0) {
   const int32_t lo = a - c0, hi = b - c0;
