@@ -41,7 +41,12 @@
 
 namespace rcp {
 
-constexpr int kPfThreads = 224;   // 0 key copies, 1 MMAs, 2-5 softmax, 6 value copies
+// 0 key copies, 1 MMAs, 2-5 softmax, 6 value copies; MOD: 2-9 softmax (two threads per query
+// row, each with half of a tile's keys), 10 value copies
+template <bool MOD>
+constexpr int pf_threads() {
+  return MOD ? 352 : 224;
+}
 constexpr float kPfRescale = 8.f;   // log2 units: weights stay below 2^8 between rescales
 
 // RECON: the values are the reconstructed V^ rows of head h (N = d) instead of a slice
@@ -73,9 +78,11 @@ struct PfSmem {
   static constexpr int BAR_OFF = END;                   // NBAR mbarriers
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;   // tmem slot, abort flag
   // MOD: least and largest first token of the tile's rows (per warp), the rejected pages of
-  // each key stage and of each score buffer, and the softmax warps' column masks [2][4][4]
+  // each key stage and of each score buffer, the softmax warps' column masks [2][4][4] and the
+  // row halves' maxima [HB][2][128] (the rank-space variant has room for one buffer)
   static constexpr int MOD_OFF = MISC_OFF + 16;
-  static constexpr int MOD_BYTES = MOD ? (8 + 8 + 2 + 2 * 16) * 4 : 0;
+  static constexpr int HB = RECON ? 2 : 1;
+  static constexpr int MOD_BYTES = MOD ? (8 + 8 + 2 + 2 * 16 + HB * 2 * 128) * 4 : 0;
   static constexpr int TOTAL = MOD_OFF + MOD_BYTES;
   static constexpr int ALLOC = TOTAL + 1024;
   static constexpr int RPC = 128 / NQ;                  // output rows each slice CTA sums
@@ -91,7 +98,7 @@ struct PfSmem {
 // its rows on; each row masks its scores to what it sees, and a key that no row of the tile
 // sees has its value row zeroed.
 template <class S, bool RECON, bool MOD>
-__global__ void __launch_bounds__(kPfThreads, 1)
+__global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qhi_map,
                    const __grid_constant__ CUtensorMap qlo_map,
                    const __grid_constant__ CUtensorMap kp_map,
@@ -140,6 +147,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   int* kbad = wlo + 8;                                  // MOD [8]: rejected pages of a tile
   int* sbad = kbad + 8;                                 // MOD [2]: the same per score buffer
   uint32_t* colm = reinterpret_cast<uint32_t*>(sbad + 2);   // MOD [2][4][4]
+  float* half_max = reinterpret_cast<float*>(colm + 32);    // MOD [HB][2][128]
+  constexpr int NSW = MOD ? 8 : 4;                          // softmax warps 2 .. NSW + 1
+  constexpr int HALVES = NSW / 4;                           // threads per query row
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -152,11 +162,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     mbar_init(&s_full[0], MOD ? 2 : 1);   // the commit (MOD: and the MMA thread, after sbad)
     mbar_init(&s_full[1], MOD ? 2 : 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], NSW);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(acc_done, 1);
-    mbar_init(zq_full, 4);
+    mbar_init(zq_full, NSW);
     mbar_init(w_full, 1);
     mbar_init(o_done, 1);
     *abort_flag = 0;
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tma_load_2d(sm + L::ST_OFF + s * L::STAGE + lane * 2048, &kp_map, 0,
                     (phys * H + h) * kBlockSize, &k_full[s]);
     }
-  } else if (warp == 6) {
+  } else if (warp == 2 + NSW) {
     // ---------------------------------------------------------------- value copies
     if constexpr (RECON) {
       // V^ rows of the request are contiguous: one 64-column box of 128 keys per group
@@ -397,8 +407,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
     }
   } else {
-    // ----------------------------------------------- softmax (one thread per query row)
+    // ----------------------------------------------- softmax (one thread per query row, or
+    // MOD two: with the extra arithmetic per score one warp per scheduler set the pace)
     const int quarter = warp & 3;
+    const int hf = (warp - 2) >> 2;                     // MOD: half of the tile's keys
+    constexpr int KC = KT / HALVES, VC = VN / HALVES;   // this thread's keys, value columns
     const int r = quarter * 32 + lane;                  // query row within the tile
     const int ci = i0 + r;                              // chunk row
     const bool row_ok = ci < n;
@@ -422,14 +435,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc_fence_after();
       const int lim = row_ok ? pos - j * KT : -1;       // columns 0 .. lim are valid
       // the whole 128-column score row: eight loads in flight, one wait
-      float sv[KT];
+      float sv[KC];
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < KT; c += 16)
-          tmem_ld16(tl + s * 128 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+        for (int c = 0; c < KC; c += 16)
+          tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
         tmem_wait_ld();
       }
-      const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key
+      const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key,
+      const int h0 = t0 + hf * KC;                      // ... and this thread's
       uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
       float shift = 0.f;                                // MOD: to be added to every score
       if constexpr (MOD) {
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (!far) {
             float vmax = 0.f;
 #pragma unroll
-            for (int c = 0; c < KT; c += 2) {
+            for (int c = 0; c < KC; c += 2) {
               const float2 y = cap_pair_near(make_float2(sv[c], sv[c + 1]), p.inv_cap2, vmax);
               sv[c] = y.x;
               sv[c + 1] = y.y;
@@ -447,14 +461,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               // still in tensor memory; the warp stays with the general form from here on
               far = true;
 #pragma unroll
-              for (int c = 0; c < KT; c += 16)
-                tmem_ld16(tl + s * 128 + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+              for (int c = 0; c < KC; c += 16)
+                tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
               tmem_wait_ld();
             }
           }
           if (far) {
 #pragma unroll
-            for (int c = 0; c < KT; c += 2) {
+            for (int c = 0; c < KC; c += 2) {
               const float2 y = cap_pair_far(make_float2(sv[c], sv[c + 1]), p.cap2, p.inv_cap2);
               sv[c] = y.x;
               sv[c + 1] = y.y;
@@ -462,15 +476,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
         if (ok && p.slopes) {
-          if (__all_sync(0xffffffffu, t0 + KT - 1 <= org)) {
+          if (__all_sync(0xffffffffu, h0 + KC - 1 <= org)) {
             // every key at or before the origin: slope (t - org), its tile-wide part kept apart
-            shift = slope2 * static_cast<float>(t0 - org);
+            shift = slope2 * static_cast<float>(h0 - org);
 #pragma unroll
-            for (int c = 0; c < KT; ++c) sv[c] = fmaf(slope2, static_cast<float>(c), sv[c]);
+            for (int c = 0; c < KC; ++c) sv[c] = fmaf(slope2, static_cast<float>(c), sv[c]);
           } else {
-            const float d0 = static_cast<float>(org - t0);
+            const float d0 = static_cast<float>(org - h0);
 #pragma unroll
-            for (int c = 0; c < KT; ++c)
+            for (int c = 0; c < KC; ++c)
               sv[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
           }
         }
@@ -479,12 +493,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const bool whole = bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
         if (!ok || !row_ok || !whole) {
 #pragma unroll
-          for (int k = 0; k < KT / 32; ++k) {
+          for (int k = 0; k < KC / 32; ++k) {
             uint32_t w = 0;
             if (ok && row_ok) {
-              w = column_bits(0, view.pfx, t0 + 32 * k) | column_bits(view.lo, pos + 1, t0 + 32 * k);
-              if ((bad >> (2 * k)) & 1u) w &= 0xFFFF0000u;
-              if ((bad >> (2 * k)) & 2u) w &= 0x0000FFFFu;
+              const uint32_t pages = bad >> ((hf * KC + 32 * k) / kBlockSize);
+              w = column_bits(0, view.pfx, h0 + 32 * k) | column_bits(view.lo, pos + 1, h0 + 32 * k);
+              if (pages & 1u) w &= 0xFFFF0000u;
+              if (pages & 2u) w &= 0x0000FFFFu;
             }
 #pragma unroll
             for (int c = 0; c < 32; ++c) sv[32 * k + c] = (w >> c) & 1u ? sv[32 * k + c] : -INFINITY;
@@ -494,11 +509,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!whole) {   // uniform over the softmax warps
           uint32_t* cm = colm + s * 16;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < KC / 32; ++k) {
             const uint32_t w = __reduce_or_sync(0xffffffffu, unseen[k]);
-            if (lane == 0) cm[quarter * 4 + k] = w;
+            if (lane == 0) cm[quarter * 4 + hf * (KC / 32) + k] = w;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1, 32 * NSW);
 #pragma unroll
           for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
         } else {
@@ -511,25 +526,33 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // the max and the exponentials below need no per-element test (exp2(-inf) = 0)
       if (!MOD && (!ok || !full_tile)) {
 #pragma unroll
-        for (int c = 0; c < KT; ++c) sv[c] = (ok && c <= lim) ? sv[c] : -INFINITY;
+        for (int c = 0; c < KC; ++c) sv[c] = (ok && c <= lim) ? sv[c] : -INFINITY;
       }
       // row max: four independent chains of three-input maxima
       float mx;
       {
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < KT; c += 8) {
+        for (int c = 0; c < KC; c += 8) {
           m4[0] = max3f(m4[0], sv[c], sv[c + 1]);
           m4[1] = max3f(m4[1], sv[c + 2], sv[c + 3]);
           m4[2] = max3f(m4[2], sv[c + 4], sv[c + 5]);
           m4[3] = max3f(m4[3], sv[c + 6], sv[c + 7]);
         }
         mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-        if constexpr (MOD) mx += shift;
+        if constexpr (MOD) {
+          // the row's largest: this half's and the other's
+          mx += shift;
+          float* hm = half_max + (L::HB > 1 ? s * 256 : 0);
+          if (L::HB == 1) named_bar_sync(2, 32 * NSW);   // the last tile's have been read
+          hm[hf * 128 + r] = mx;
+          named_bar_sync(2, 32 * NSW);
+          mx = fmaxf(mx, hm[(hf ^ 1) * 128 + r]);
+        }
       }
       const float m_new = (mx > m_run + kPfRescale) ? mx : m_run;
       const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
-      uint32_t packed[KT / 2];
+      uint32_t packed[KC / 2];
       float rsum;
       {
         // rows with no valid key
@@ -541,7 +564,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // the row sum is taken in fp32 before the weights are rounded to fp16; pairs of
         // columns go through the packed fp32x2 add / subtract
 #pragma unroll
-        for (int c = 0; c < KT; c += 2) {
+        for (int c = 0; c < KC; c += 2) {
           const float2 d = sub_f32x2(make_float2(sv[c], sv[c + 1]), msub2);
           const float2 pp = make_float2(fast_exp2(d.x), fast_exp2(d.y));
           s4[(c >> 1) & 3] = add_f32x2(s4[(c >> 1) & 3], pp);
@@ -568,7 +591,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // (lanes whose max did not move multiply by 1)
       if (ok && rescale) {
 #pragma unroll 1
-        for (int c = 0; c < VN; c += 32) {
+        for (int c = hf * VC; c < (hf + 1) * VC; c += 32) {
           float v[16], w[16];
           tmem_ld16(tl + 256 + c, v);
           tmem_ld16(tl + 256 + c + 16, w);
@@ -587,14 +610,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // P row r into tensor memory lane r: column c holds keys 2c and 2c+1
         if (ok) {
 #pragma unroll
-          for (int c = 0; c < KT / 2; c += 16) tmem_st16u(tl + L::P_TM + (j & 1) * (KT / 2) + c, &packed[c]);
+          for (int c = 0; c < KC / 2; c += 16)
+            tmem_st16u(tl + L::P_TM + (j & 1) * (KT / 2) + hf * (KC / 2) + c, &packed[c]);
           tmem_wait_st();
         }
       } else {
         // P row r, K-major, 128-byte swizzle: 16-byte chunk c of the row sits at c ^ (r % 8)
 #pragma unroll
-        for (int ch = 0; ch < KT / 8; ++ch) {
-          const int kb = ch >> 3, cc = ch & 7;
+        for (int ch = 0; ch < KC / 8; ++ch) {
+          const int kb = (hf * (KC / 8) + ch) >> 3, cc = ch & 7;
           *reinterpret_cast<uint4*>(pbuf + kb * 16384 + r * 128 + ((cc ^ (r & 7)) << 4)) =
               make_uint4(packed[ch * 4], packed[ch * 4 + 1], packed[ch * 4 + 2], packed[ch * 4 + 3]);
         }
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // keys that no row sees (among them tokens past the end and rejected pages): the same
         ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
         uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
-        for (int idx = threadIdx.x - 64; idx < KT * NG * 8; idx += 128) {   // warps 2-5
+        for (int idx = threadIdx.x - 64; idx < KT * NG * 8; idx += 32 * NSW) {
           const int tok = idx / (NG * 8);
           const uint32_t w = tok < 64 ? (tok < 32 ? unseen[0] : unseen[1])
                                       : (tok < 96 ? unseen[2] : unseen[3]);
@@ -638,13 +662,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag, p.dev_err));
     tc_fence_after();
+    if constexpr (MOD) {   // the halves' sums (every thread is done with its last tile)
+      float* hm = half_max;
+      hm[hf * 128 + r] = l_run;
+      named_bar_sync(2, 32 * NSW);
+      l_run += hm[(hf ^ 1) * 128 + r];
+    }
     const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
     if constexpr (RECON) {
       // ------------------------------------------- O / l straight to the output rows
       if (ok) {   // warp-uniform: every lane loads, only rows of the chunk are stored
         __half* dst = static_cast<__half*>(p.out) + (static_cast<size_t>(row0 + r) * H + h) * D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = hf * (D / HALVES); c < (hf + 1) * (D / HALVES); c += 16) {
           float v[16];
           tmem_ld16(tl + 256 + c, v);
           tmem_wait_ld();
@@ -666,7 +696,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       uint8_t* zh = sm + L::ZH_OFF;
       uint8_t* zl = sm + L::ZL_OFF;
 #pragma unroll 1
-      for (int c = 0; c < RQ; c += 32) {
+      for (int c = hf * (RQ / HALVES); c < (hf + 1) * (RQ / HALVES); c += 32) {
         float v[32];
         if (ok) {
           tmem_ld16(tl + 256 + c, *reinterpret_cast<float(*)[16]>(&v[0]));
@@ -762,7 +792,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
     }
     cluster_sync_all();
-    for (int idx = threadIdx.x; idx < RPC * D / 2; idx += kPfThreads) {
+    for (int idx = threadIdx.x; idx < RPC * D / 2; idx += pf_threads<MOD>()) {
       const int rr = idx / (D / 2), d2 = (idx % (D / 2)) * 2;
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
@@ -805,7 +835,7 @@ cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const
   const int NQ = recon ? 1 : PrefillCfg<S>::NQ;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(max_tiles * S::H * NQ);
-  cfg.blockDim = dim3(kPfThreads);
+  cfg.blockDim = dim3(p.mod ? pf_threads<true>() : pf_threads<false>());
   cfg.dynamicSmemBytes = p.mod ? (recon ? PfSmem<S, true, true>::ALLOC : PfSmem<S, false, true>::ALLOC)
                                : (recon ? PfSmem<S, true>::ALLOC : PfSmem<S, false>::ALLOC);
   cfg.stream = stream;
