@@ -163,7 +163,7 @@ class ScoreMod:
     t > pos - window, with scores softcap * tanh(s / softcap) - alibi_slopes[h] * |pos - t|.
     What is left at 0 / None takes no part.
 
-    softcap: 0, or between 2**-10 and 2**20; window: tokens, the row's own included;
+    softcap: 0, or between 2**-10 and 2**16; window: tokens, the row's own included;
     alibi_slopes: [H] float32; prefix_lens: [B] int32; row_begin: [query rows] int32 (decode: [B],
     a document mask's start of the row's document).  The tensors are read by the kernels, on
     the call's stream.

@@ -203,8 +203,14 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     lt = max(lt, npt);
     nkt = npt + max(0, nkt - lt);
   }
-  // key tile number j of this CTA
-  auto tile_of = [&](int j) { return MOD && j >= npt ? lt + (j - npt) : j; };
+  // key tile number j of this CTA.  MOD: the nearest first, so that under a bias the running
+  // maximum settles with the first tile (it would grow, and the accumulator be rescaled, with
+  // every tile that comes nearer)
+  auto tile_of = [&](int j) {
+    if (!MOD) return j;
+    const int i = nkt - 1 - j;
+    return i >= npt ? lt + (i - npt) : i;
+  };
   // whether page x of the request is read (MOD: some row of the tile may see it)
   auto page_read = [&](int x) {
     return x < nblk && (!MOD || x * kBlockSize < pfx || (x + 1) * kBlockSize > lo_min);
@@ -421,6 +427,7 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     // MOD: what this row sees, its head's bias per token (log2 units) and where it starts from
     RowView view{pfx, 0};
     bool far = false;          // a score passed the range of the cap's polynomial
+    const CapNear near(p.cap2, p.inv_cap2);
     int32_t org = 0;
     float slope2 = 0.f;
     if constexpr (MOD) {
@@ -447,18 +454,40 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
       uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
       float shift = 0.f;                                // MOD: to be added to every score
       if constexpr (MOD) {
+        // a tile that every row of the CTA sees whole needs no mask
+        const uint32_t bad = static_cast<uint32_t>(sbad[s]);
+        const bool whole = bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
+        const bool edge = !ok || !row_ok || !whole;
+        if (edge) {
+#pragma unroll
+          for (int k = 0; k < KC / 32; ++k) {
+            uint32_t w = 0;
+            if (ok && row_ok) {
+              const uint32_t pages = bad >> ((hf * KC + 32 * k) / kBlockSize);
+              w = column_bits(0, view.pfx, h0 + 32 * k) | column_bits(view.lo, pos + 1, h0 + 32 * k);
+              if (pages & 1u) w &= 0xFFFF0000u;
+              if (pages & 2u) w &= 0x0000FFFFu;
+            }
+            unseen[k] = w;   // keys this row sees, until the rows are joined below
+          }
+        }
         if (ok && p.cap2 > 0.f) {
           if (!far) {
-            float vmax = 0.f;
+            // which form the cap takes must not depend on what hidden slots hold
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < KC; ++c) sv[c] = (unseen[c / 32] >> (c % 32)) & 1u ? sv[c] : 0.f;
+            }
+            float wmax = 0.f;
 #pragma unroll
             for (int c = 0; c < KC; c += 2) {
-              const float2 y = cap_pair_near(make_float2(sv[c], sv[c + 1]), p.inv_cap2, vmax);
+              const float2 y = cap_pair_near(make_float2(sv[c], sv[c + 1]), near, wmax);
               sv[c] = y.x;
               sv[c + 1] = y.y;
             }
-            if (__any_sync(0xffffffffu, !(vmax <= kCapNear))) {
-              // some score is past the polynomial's range (or NaN): the tile's scores are
-              // still in tensor memory; the warp stays with the general form from here on
+            if (__any_sync(0xffffffffu, !(wmax <= near.w_near))) {
+              // some score is past the polynomial's range: the tile's scores are still in
+              // tensor memory; the warp stays with the general form from here on
               far = true;
 #pragma unroll
               for (int c = 0; c < KC; c += 16)
@@ -467,9 +496,18 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
             }
           }
           if (far) {
+            const float twice_inv = 2.88539008f * p.inv_cap2;
+            const bool large = p.cap2 > kCapLarge;   // uniform over the grid
 #pragma unroll
             for (int c = 0; c < KC; c += 2) {
-              const float2 y = cap_pair_far(make_float2(sv[c], sv[c + 1]), p.cap2, p.inv_cap2);
+              const float2 x = make_float2(sv[c], sv[c + 1]);
+              float2 y = cap_pair_far(x, p.cap2, twice_inv);
+              if (large) {
+                float w = 0.f;
+                const float2 n = cap_pair_near(x, near, w);
+                if (x.x * x.x <= near.w_near) y.x = n.x;
+                if (x.y * x.y <= near.w_near) y.y = n.y;
+              }
               sv[c] = y.x;
               sv[c + 1] = y.y;
             }
@@ -488,23 +526,9 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
               sv[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
           }
         }
-        // a tile that every row of the CTA sees whole needs no mask
-        const uint32_t bad = static_cast<uint32_t>(sbad[s]);
-        const bool whole = bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
-        if (!ok || !row_ok || !whole) {
+        if (edge) {
 #pragma unroll
-          for (int k = 0; k < KC / 32; ++k) {
-            uint32_t w = 0;
-            if (ok && row_ok) {
-              const uint32_t pages = bad >> ((hf * KC + 32 * k) / kBlockSize);
-              w = column_bits(0, view.pfx, h0 + 32 * k) | column_bits(view.lo, pos + 1, h0 + 32 * k);
-              if (pages & 1u) w &= 0xFFFF0000u;
-              if (pages & 2u) w &= 0x0000FFFFu;
-            }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) sv[32 * k + c] = (w >> c) & 1u ? sv[32 * k + c] : -INFINITY;
-            unseen[k] = w;   // keys this row sees, until the rows are joined below
-          }
+          for (int c = 0; c < KC; ++c) sv[c] = (unseen[c / 32] >> (c % 32)) & 1u ? sv[c] : -INFINITY;
         }
         if (!whole) {   // uniform over the softmax warps
           uint32_t* cm = colm + s * 16;

@@ -71,33 +71,41 @@ struct TileMap {
 };
 
 // cap2 tanh(x / cap2) of a pair of scores, log2 units, for the prefill, where a row meets 128
-// of them per tile.  Scores well below the cap (|x| <= 0.7 cap2) take a polynomial: with
-// u = x / cap2 and v = u^2, tanh(u) / u = 1 + v q(v), q the least-maximum fit of degree 3 on
-// v in [0, 0.49] (relative error 3.2e-7).  vmax collects the largest v; the caller goes to
-// cap_pair_far if it passed kCapNear.
-constexpr float kCapNear = 0.49f;
+// of them per tile and the FMA pipe sets the pace: six operations per score.  Scores up to 0.7
+// of the cap take a polynomial: with u = x / cap2 and v = u^2, tanh(u) / u = 1 + v q(v), q the
+// least-maximum fit of degree 3 on v in [0, 0.49] (relative error 3.2e-7, absolute 2.7e-7 of
+// the cap).  CapNear holds its coefficients in powers of x^2, c_k / cap2^(2k), within fp32 for
+// every cap allowed.  wmax collects the largest x^2; the caller takes cap_far if it passed
+// w_near = (0.7 cap2)^2.
+struct CapNear {
+  float c1, c2, c3, c4, w_near;
+  __device__ __forceinline__ explicit CapNear(float cap2, float inv_cap2) {
+    const float i2 = inv_cap2 * inv_cap2;
+    c1 = -0.333311808f * i2;
+    c2 = 0.132888389f * i2 * i2;
+    c3 = -0.0510577062f * i2 * i2 * i2;
+    c4 = 0.013981962f * i2 * i2 * i2 * i2;
+    w_near = 0.49f * cap2 * cap2;
+  }
+};
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 cap_pair_near(float2 x, float inv_cap2, float& vmax) {
-  const float2 u = mul_f32x2(x, both(inv_cap2)), v = mul_f32x2(u, u);
-  float2 q = fma_f32x2(both(0.013981962f), v, both(-0.0510577062f));
-  q = fma_f32x2(q, v, both(0.132888389f));
-  q = fma_f32x2(q, v, both(-0.333311808f));
-  vmax = max3f(vmax, v.x, v.y);
-  return fma_f32x2(mul_f32x2(x, v), q, x);
+__device__ __forceinline__ float2 cap_pair_near(float2 x, const CapNear& k, float& wmax) {
+  const float2 w = mul_f32x2(x, x);
+  float2 q = fma_f32x2(both(k.c4), w, both(k.c3));
+  q = fma_f32x2(q, w, both(k.c2));
+  q = fma_f32x2(q, w, both(k.c1));
+  wmax = max3f(wmax, w.x, w.y);
+  return fma_f32x2(mul_f32x2(x, w), q, x);
 }
-// Any score: 1 - 2 / (e^2u + 1) past the polynomial's range (absolute error about 3e-7 of the
-// cap, below 7e-7 of the result there), the polynomial within it.
-__device__ __forceinline__ float cap_far(float x, float cap2, float inv_cap2) {
-  const float e = fast_exp2(x * inv_cap2 * 2.88539008f);
-  return fmaf(-2.f * cap2, fast_rcp(e + 1.f), cap2);
-}
-__device__ __forceinline__ float2 cap_pair_far(float2 x, float cap2, float inv_cap2) {
-  float vx = 0.f, vy = 0.f;
-  const float2 n = cap_pair_near(x, inv_cap2, vx);
-  vx = x.x * inv_cap2;
-  vy = x.y * inv_cap2;
-  return make_float2(vx * vx <= kCapNear ? n.x : cap_far(x.x, cap2, inv_cap2),
-                     vy * vy <= kCapNear ? n.y : cap_far(x.y, cap2, inv_cap2));
+// Any score: 1 - 2 / (e^2u + 1), absolute error about 3e-7 of the cap as well (the two
+// approximate instructions' 2^-22 and 2^-23).  Under a cap so large that this is more than a
+// score's own rounding matters (cap2 > 128: beyond 4e-5) scores up to 0.7 of it take the
+// polynomial.
+constexpr float kCapLarge = 128.f;
+__device__ __forceinline__ float2 cap_pair_far(float2 x, float cap2, float twice_inv) {
+  const float2 a = mul_f32x2(x, both(twice_inv));   // twice_inv = 2 log2(e) / cap2
+  const float2 e = add_f32x2(make_float2(fast_exp2(a.x), fast_exp2(a.y)), both(1.f));
+  return fma_f32x2(make_float2(fast_rcp(e.x), fast_rcp(e.y)), both(-2.f * cap2), both(cap2));
 }
 
 // Bits c of a 32-column word starting at column c0 whose columns lie in [a, b).
