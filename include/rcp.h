@@ -269,7 +269,7 @@ rcp_status rcp_prefill_crossover_rows(const rcp_cache* cache, int32_t* rows);
  *     s = q~_h . c_k[t,h] / sqrt(d);   s = softcap tanh(s / softcap);
  *     s = s - alibi_slopes[h] |pos - t|.
  * A row that sees no token gives zeros.  A zero or NULL member leaves its part out:
- *   softcap       cap of the scores, 0 or in [2^-10, 2^16];
+ *   softcap       cap of the scores, 0 or in [2^-10, 2^10];
  *   alibi_slopes  [H] fp32 device, finite: a bias that falls with the distance;
  *   window        >= 0: the last `window` tokens up to and including the row's own;
  *   prefix_lens   [batch] int32 device: tokens that every row of the request sees, whatever

@@ -163,7 +163,7 @@ class ScoreMod:
     t > pos - window, with scores softcap * tanh(s / softcap) - alibi_slopes[h] * |pos - t|.
     What is left at 0 / None takes no part.
 
-    softcap: 0, or between 2**-10 and 2**16; window: tokens, the row's own included;
+    softcap: 0, or between 2**-10 and 2**10; window: tokens, the row's own included;
     alibi_slopes: [H] float32; prefix_lens: [B] int32; row_begin: [query rows] int32 (decode: [B],
     a document mask's start of the row's document).  The tensors are read by the kernels, on
     the call's stream.
@@ -442,7 +442,13 @@ class PagedCoeffCache:
             ws.numel() * ws.element_size(), _stream(stream)))
         return out
 
-    def _prefill_variant(self, variant: str, rows: int, B: int) -> str:
+    def _prefill_variant(self, variant: str, rows: int, B: int, mod=None) -> str:
+        if variant == "auto" and mod is not None:
+            # one 128-row tile is 128 rank-space CTAs, one wave of the SMs; measured with capped
+            # scores, rank space against reconstruction: one request of up to 8 rows 37 / 42 us
+            # behind 777 tokens, 91 / 112 behind 4096, 613 / 762 behind 32768; four of them
+            # 120 / 57, 337 / 197 and 2348 / 1439
+            variant = "rank" if self.page_format == "fp16" and B == 1 and rows <= 128 else "reconstruct"
         if variant == "auto":
             variant = "reconstruct" if (self.page_format != "fp16" or
                                         (B > 0 and rows >= B * RECONSTRUCT_MIN_CHUNK)) else "rank"
@@ -488,7 +494,7 @@ class PagedCoeffCache:
         rows, B = _validate_prefill(self.device, H, d, q, cu_chunk_lens, block_table, seq_lens,
                                     out)
         mb = int(block_table.shape[1])
-        variant = self._prefill_variant(variant, rows, B)
+        variant = self._prefill_variant(variant, rows, B, mod)
         ws = self._prefill_workspace(variant, rows, B, mb) if workspace is None else workspace
         if mod is not None:
             _validate_workspace(self.device, ws)
@@ -518,7 +524,7 @@ class PagedCoeffCache:
         rows, B = _validate_prefill(self.device, H, d, q, cu_chunk_lens, block_table, seq_lens,
                                     out)
         mb = int(block_table.shape[1])
-        variant = self._prefill_variant(variant, rows, B)
+        variant = self._prefill_variant(variant, rows, B, mod)
         ws = self._prefill_workspace(variant, rows, B, mb) if workspace is None else workspace
         _validate_workspace(self.device, ws)
         if mod is not None:

@@ -335,9 +335,9 @@ cudaError_t copy_pages(rcp_cache* c, const rcp::CopyParams& p, const int32_t* li
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Least and largest score caps: between them the eighth powers of cap log2(e) and of its
-// reciprocal (the prefill's polynomial) stay within fp32.
-constexpr float kMinSoftcap = 1.f / 1024, kMaxSoftcap = 65536.f;
+// Least and largest score caps: the eighth power of the least one's reciprocal (the prefill's
+// polynomial) stays within fp32, the largest one's error within a weight's rounding.
+constexpr float kMinSoftcap = 1.f / 1024, kMaxSoftcap = 1024.f;
 
 rcp_status check_mod(const rcp_score_mod& m) {
   if (!(m.softcap == 0.f || (m.softcap >= kMinSoftcap && m.softcap <= kMaxSoftcap)))   // NaN too

@@ -41,12 +41,14 @@
 
 namespace rcp {
 
-// 0 key copies, 1 MMAs, 2-5 softmax, 6 value copies; MOD: 2-9 softmax (two threads per query
-// row, each with half of a tile's keys), 10 value copies
+// Warps: 0 key copies, 1 MMAs, then the softmax warps and one for the value copies.
+//   plain  2-5 softmax (one thread per query row), 6 value copies
+//   MOD    2-9 softmax (two threads per row, each with half of a tile's keys), 10
 template <bool MOD>
-constexpr int pf_threads() {
-  return MOD ? 352 : 224;
-}
+struct PfWarps {
+  static constexpr int NSW = MOD ? 8 : 4;
+  static constexpr int THREADS = 32 * (3 + NSW);
+};
 constexpr float kPfRescale = 8.f;   // log2 units: weights stay below 2^8 between rescales
 
 // RECON: the values are the reconstructed V^ rows of head h (N = d) instead of a slice
@@ -98,7 +100,7 @@ struct PfSmem {
 // its rows on; each row masks its scores to what it sees, and a key that no row of the tile
 // sees has its value row zeroed.
 template <class S, bool RECON, bool MOD>
-__global__ void __launch_bounds__(pf_threads<MOD>(), 1)
+__global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qhi_map,
                    const __grid_constant__ CUtensorMap qlo_map,
                    const __grid_constant__ CUtensorMap kp_map,
@@ -148,7 +150,8 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
   int* sbad = kbad + 8;                                 // MOD [2]: the same per score buffer
   uint32_t* colm = reinterpret_cast<uint32_t*>(sbad + 2);   // MOD [2][4][4]
   float* half_max = reinterpret_cast<float*>(colm + 32);    // MOD [HB][2][128]
-  constexpr int NSW = MOD ? 8 : 4;                          // softmax warps 2 .. NSW + 1
+  using W = PfWarps<MOD>;
+  constexpr int NSW = W::NSW;                               // softmax warps 2 .. NSW + 1
   constexpr int HALVES = NSW / 4;                           // threads per query row
 
   if (threadIdx.x == 0) {
@@ -217,6 +220,23 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
   };
   if constexpr (NQ > 1) cluster_sync_all();   // peers are running before any remote store
 
+  // MOD: a tile that every row of the CTA sees whole needs no mask
+  auto sees_whole = [&](int t0, uint32_t bad) {
+    return bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
+  };
+  // MOD: zeroes the value rows of tile j's keys whose bit is set, by n threads (this one: tid)
+  auto zero_values = [&](int j, const uint32_t (&keys)[4], int tid, int n) {
+    uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
+    for (int idx = tid; idx < KT * NG * 8; idx += n) {
+      const int tok = idx / (NG * 8);
+      const uint32_t w = tok < 64 ? (tok < 32 ? keys[0] : keys[1]) : (tok < 96 ? keys[2] : keys[3]);
+      if (!((w >> (tok & 31)) & 1u)) continue;
+      const int rem = idx % (NG * 8);
+      const int g = rem >> 3, ch = rem & 7;
+      *reinterpret_cast<uint4*>(vst + (g * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
+                                (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+    }
+  };
   if (warp == 0) {
     // ------------------------------------------------------------------ key copies
     // The whole warp: lane jb < 8 resolves page jb of each tile one tile ahead and issues
@@ -324,75 +344,147 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     // of tile jp once its weights are written and its values landed.  The tensor pipe
     // runs them in order, so S(j+1) overlaps the softmax of tile j and PV(j) overlaps
     // the softmax of tile j+1.
-    if (lane == 0) {
+    if constexpr (MOD) {
+      // S(0), S(1), then PV(j) and S(j + 2) in turn.  The whole warp runs the loop and one
+      // elected lane issues, which leaves the descriptors in uniform registers, and the waits
+      // block instead of polling: with the loop below a tile's two products took 2200 cycles
+      // from weights to scores, as long as its softmax, now 1700.
+      constexpr uint32_t id_s = make_idesc_f16(128, KT, false, false);
+      constexpr uint32_t id_pv = make_idesc_f16(128, VN, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t qd = make_sdesc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t pd = make_sdesc(smem_u32(sm + L::P_OFF), 16, 1024, kSwizzle128B);
+      const uint64_t kd0 = make_sdesc(smem_u32(sm + L::ST_OFF), 16, 1024, kSwizzle128B);
+      const uint64_t vd0 = make_sdesc(smem_u32(sm + L::ST_OFF + L::K_BYTES),
+                                      (KT / kBlockSize) * 2048, 1024, kSwizzle128B);
+      int ks = 0, vs = 0;                // stages of the next keys and values
+      uint32_t kph = 0, vph = 0;         // their phases
+      const bool leader = elect_one();
+      auto scores = [&](int j) {
+        const int g = j & 1;
+        const bool go = mbar_wait(&k_full[ks], kph, abort_flag, p.dev_err);
+        if (!__all_sync(0xffffffffu, go)) return false;
+        tc_fence_after();
+        const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (L::STAGE >> 4));
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            umma_f16(tm + g * 128, qd + kk * 2, kd + kk * 2, id_s, kk > 0 ? 1u : 0u);
+            umma_f16(tm + g * 128, qd + (L::Q_BYTES >> 4) + kk * 2, kd + kk * 2, id_s, 1u);
+          }
+          sbad[g] = kbad[j & 7];
+          mbar_arrive(&s_full[g]);
+          umma_commit(&s_full[g]);
+          umma_commit(&k_empty[ks]);
+        }
+        __syncwarp();
+        if (++ks == NS) {
+          ks = 0;
+          kph ^= 1;
+        }
+        return true;
+      };
+      bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.dev_err));
+      ok = ok && (nkt < 1 || scores(0)) && (nkt < 2 || scores(1));
+      for (int j = 0; ok && j < nkt; ++j) {
+        // RECON: P buffer j & 1, each with its own barriers; rank space: one P buffer
+        const int pb = RECON ? (j & 1) : 0;
+        ok = mbar_wait(&v_full[vs], vph, abort_flag, p.dev_err);
+        ok = mbar_wait(&p_full[pb], RECON ? (j >> 1) & 1 : j & 1, abort_flag, p.dev_err) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (L::STAGE >> 4));
+        const uint32_t more = j > 0 ? 1u : 0u;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k) {
+            if constexpr (RECON)
+              umma_f16_ta(tm + 256, tm + L::P_TM + pb * (KT / 2) + k * 8, vd + k * (2048 >> 4), id_pv,
+                          k > 0 ? 1u : more);
+            else
+              umma_f16(tm + 256, pd + (k >> 2) * (16384 >> 4) + (k & 3) * 2, vd + k * (2048 >> 4),
+                       id_pv, k > 0 ? 1u : more);
+          }
+          umma_commit(&pv_done[pb]);
+          umma_commit(&v_empty[vs]);
+        }
+        __syncwarp();
+        if (++vs == NS) {
+          vs = 0;
+          vph ^= 1;
+        }
+        if (j + 2 < nkt) ok = scores(j + 2);
+      }
+      if (leader) umma_commit(acc_done);
+    }
+    if (!(MOD && RECON) && lane == 0) {
       constexpr uint32_t id_s = make_idesc_f16(128, KT, false, false);
       constexpr uint32_t id_pv = make_idesc_f16(128, VN, false, true);
       constexpr uint32_t id_o = make_idesc_f16(128, D, false, true);
       const uint32_t qa = smem_u32(sm);
       const uint32_t pa = smem_u32(sm + L::P_OFF);
-      bool ok = mbar_wait(q_full, 0, abort_flag, p.dev_err);
-      int js = 0, jp = 0;
-      uint64_t t_idle = 0;
-      while (ok && jp < nkt) {
-        bool progress = false;
-        if (js < nkt && js <= jp + 1 && mbar_test_wait(&k_full[js % NS], (js / NS) & 1)) {
-          tc_fence_after();
-          const uint32_t ka = smem_u32(sm + L::ST_OFF + (js % NS) * L::STAGE);
+      if constexpr (!MOD) {
+        bool ok = mbar_wait(q_full, 0, abort_flag, p.dev_err);
+        int js = 0, jp = 0;
+        uint64_t t_idle = 0;
+        while (ok && jp < nkt) {
+          bool progress = false;
+          if (js < nkt && js <= jp + 1 && mbar_test_wait(&k_full[js % NS], (js / NS) & 1)) {
+            tc_fence_after();
+            const uint32_t ka = smem_u32(sm + L::ST_OFF + (js % NS) * L::STAGE);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t bd = make_sdesc(ka + kk * 32, 16, 1024, kSwizzle128B);
-            umma_f16(tmem + (js & 1) * 128, make_sdesc(qa + kk * 32, 16, 1024, kSwizzle128B), bd,
-                     id_s, kk > 0 ? 1u : 0u);
-            umma_f16(tmem + (js & 1) * 128,
-                     make_sdesc(qa + L::Q_BYTES + kk * 32, 16, 1024, kSwizzle128B), bd, id_s, 1u);
-          }
-          if constexpr (MOD) {
-            sbad[js & 1] = kbad[js & 7];
-            mbar_arrive(&s_full[js & 1]);
-          }
-          umma_commit(&s_full[js & 1]);
-          umma_commit(&k_empty[js % NS]);
-          ++js;
-          progress = true;
-        }
-        // RECON: P buffer jp & 1, each with its own barriers; rank space: one P buffer
-        const int pb = RECON ? (jp & 1) : 0;
-        const uint32_t pph = RECON ? (jp >> 1) & 1 : jp & 1;
-        if (jp < js && mbar_test_wait(&p_full[pb], pph) &&
-            mbar_test_wait(&v_full[jp % NS], (jp / NS) & 1)) {
-          tc_fence_after();
-          const uint32_t va = smem_u32(sm + L::ST_OFF + (jp % NS) * L::STAGE + L::K_BYTES);
-#pragma unroll
-          for (int ks = 0; ks < KT / 16; ++ks) {
-            const uint64_t bd = make_sdesc(va + ks * 2048, (KT / kBlockSize) * 2048, 1024,
-                                           kSwizzle128B);
-            if constexpr (RECON) {
-              umma_f16_ta(tmem + 256, tmem + L::P_TM + pb * (KT / 2) + ks * 8, bd, id_pv,
-                          (jp > 0 || ks > 0) ? 1u : 0u);
-            } else {
-              const uint64_t ad = make_sdesc(pa + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024,
-                                             kSwizzle128B);
-              umma_f16(tmem + 256, ad, bd, id_pv, (jp > 0 || ks > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t bd = make_sdesc(ka + kk * 32, 16, 1024, kSwizzle128B);
+              umma_f16(tmem + (js & 1) * 128, make_sdesc(qa + kk * 32, 16, 1024, kSwizzle128B), bd,
+                       id_s, kk > 0 ? 1u : 0u);
+              umma_f16(tmem + (js & 1) * 128,
+                       make_sdesc(qa + L::Q_BYTES + kk * 32, 16, 1024, kSwizzle128B), bd, id_s, 1u);
             }
+            umma_commit(&s_full[js & 1]);
+            umma_commit(&k_empty[js % NS]);
+            ++js;
+            progress = true;
           }
-          umma_commit(&pv_done[pb]);
-          umma_commit(&v_empty[jp % NS]);
-          ++jp;
-          progress = true;
+          // RECON: P buffer jp & 1, each with its own barriers; rank space: one P buffer
+          const int pb = RECON ? (jp & 1) : 0;
+          const uint32_t pph = RECON ? (jp >> 1) & 1 : jp & 1;
+          if (jp < js && mbar_test_wait(&p_full[pb], pph) &&
+              mbar_test_wait(&v_full[jp % NS], (jp / NS) & 1)) {
+            tc_fence_after();
+            const uint32_t va = smem_u32(sm + L::ST_OFF + (jp % NS) * L::STAGE + L::K_BYTES);
+#pragma unroll
+            for (int ks = 0; ks < KT / 16; ++ks) {
+              const uint64_t bd = make_sdesc(va + ks * 2048, (KT / kBlockSize) * 2048, 1024,
+                                             kSwizzle128B);
+              if constexpr (RECON) {
+                umma_f16_ta(tmem + 256, tmem + L::P_TM + pb * (KT / 2) + ks * 8, bd, id_pv,
+                            (jp > 0 || ks > 0) ? 1u : 0u);
+              } else {
+                const uint64_t ad = make_sdesc(pa + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024,
+                                               kSwizzle128B);
+                umma_f16(tmem + 256, ad, bd, id_pv, (jp > 0 || ks > 0) ? 1u : 0u);
+              }
+            }
+            umma_commit(&pv_done[pb]);
+            umma_commit(&v_empty[jp % NS]);
+            ++jp;
+            progress = true;
+          }
+          if (progress) {
+            t_idle = 0;
+          } else if (*abort_flag) {
+            ok = false;
+          } else if (t_idle == 0) {
+            t_idle = globaltimer_ns();
+          } else if (globaltimer_ns() - t_idle > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(p.dev_err, RCP_DEVERR_TIMEOUT);
+            ok = false;
+          }
         }
-        if (progress) {
-          t_idle = 0;
-        } else if (*abort_flag) {
-          ok = false;
-        } else if (t_idle == 0) {
-          t_idle = globaltimer_ns();
-        } else if (globaltimer_ns() - t_idle > kWaitLimitNs) {
-          *abort_flag = 1;
-          atomicOr(p.dev_err, RCP_DEVERR_TIMEOUT);
-          ok = false;
-        }
+        umma_commit(acc_done);
       }
-      umma_commit(acc_done);
       // up-projection of this slice: O = (z_hi + z_lo) W_v[slice rows, h*d:(h+1)*d]
       if (!RECON && mbar_wait(zq_full, 0, abort_flag, p.dev_err) &&
           mbar_wait(w_full, 0, abort_flag, p.dev_err)) {
@@ -416,7 +508,7 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     // ----------------------------------------------- softmax (one thread per query row, or
     // MOD two: with the extra arithmetic per score one warp per scheduler set the pace)
     const int quarter = warp & 3;
-    const int hf = (warp - 2) >> 2;                     // MOD: half of the tile's keys
+    const int hf = HALVES > 1 ? (warp - 2) >> 2 : 0;    // half of the tile's keys
     constexpr int KC = KT / HALVES, VC = VN / HALVES;   // this thread's keys, value columns
     const int r = quarter * 32 + lane;                  // query row within the tile
     const int ci = i0 + r;                              // chunk row
@@ -424,17 +516,7 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     const int pos = P0 + ci;                            // keys 0 .. pos are attended
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float m_run = -INFINITY, l_run = 0.f;
-    // MOD: what this row sees, its head's bias per token (log2 units) and where it starts from
-    RowView view{pfx, 0};
-    bool far = false;          // a score passed the range of the cap's polynomial
-    const CapNear near(p.cap2, p.inv_cap2);
-    int32_t org = 0;
-    float slope2 = 0.f;
-    if constexpr (MOD) {
-      view.lo = row_ok ? view_begin(p, row0 + r, pos) : 0;
-      org = bias_origin(view, pos);
-      slope2 = p.slopes ? p.slopes[h] * 1.44269504f : 0.f;
-    }
+    [[maybe_unused]] RowMod rm(p, h, MOD && row_ok, row0 + r, pos, pfx);
     uint8_t* pbuf = sm + L::P_OFF;
     for (int j = 0; j < nkt; ++j) {
       const int s = j & 1;
@@ -447,102 +529,41 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
 #pragma unroll
         for (int c = 0; c < KC; c += 16)
           tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
-        tmem_wait_ld();
       }
       const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key,
       const int h0 = t0 + hf * KC;                      // ... and this thread's
       uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
+      uint32_t seen[KC / 32] = {};                      // MOD: keys that this row sees (edge)
+      bool whole = true, edge = false;
       float shift = 0.f;                                // MOD: to be added to every score
-      if constexpr (MOD) {
-        // a tile that every row of the CTA sees whole needs no mask
+      if constexpr (MOD) {   // while the scores are on their way
         const uint32_t bad = static_cast<uint32_t>(sbad[s]);
-        const bool whole = bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
-        const bool edge = !ok || !row_ok || !whole;
-        if (edge) {
+        whole = sees_whole(t0, bad);
+        edge = !ok || !row_ok || !whole;
+        if (!whole && ok && row_ok) {
 #pragma unroll
-          for (int k = 0; k < KC / 32; ++k) {
-            uint32_t w = 0;
-            if (ok && row_ok) {
-              const uint32_t pages = bad >> ((hf * KC + 32 * k) / kBlockSize);
-              w = column_bits(0, view.pfx, h0 + 32 * k) | column_bits(view.lo, pos + 1, h0 + 32 * k);
-              if (pages & 1u) w &= 0xFFFF0000u;
-              if (pages & 2u) w &= 0x0000FFFFu;
-            }
-            unseen[k] = w;   // keys this row sees, until the rows are joined below
-          }
+          for (int k = 0; k < KC / 32; ++k)
+            seen[k] = rm.seen(h0 + 32 * k, bad >> ((hf * KC + 32 * k) / kBlockSize));
         }
-        if (ok && p.cap2 > 0.f) {
-          if (!far) {
-            // which form the cap takes must not depend on what hidden slots hold
-            if (edge) {
+      }
+      if (ok) tmem_wait_ld();
+      if constexpr (MOD) {
+        shift = modify_scores(sv, p, rm, h0, edge, seen, [&]() {
 #pragma unroll
-              for (int c = 0; c < KC; ++c) sv[c] = (unseen[c / 32] >> (c % 32)) & 1u ? sv[c] : 0.f;
-            }
-            float wmax = 0.f;
-#pragma unroll
-            for (int c = 0; c < KC; c += 2) {
-              const float2 y = cap_pair_near(make_float2(sv[c], sv[c + 1]), near, wmax);
-              sv[c] = y.x;
-              sv[c + 1] = y.y;
-            }
-            if (__any_sync(0xffffffffu, !(wmax <= near.w_near))) {
-              // some score is past the polynomial's range: the tile's scores are still in
-              // tensor memory; the warp stays with the general form from here on
-              far = true;
-#pragma unroll
-              for (int c = 0; c < KC; c += 16)
-                tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
-              tmem_wait_ld();
-            }
-          }
-          if (far) {
-            const float twice_inv = 2.88539008f * p.inv_cap2;
-            const bool large = p.cap2 > kCapLarge;   // uniform over the grid
-#pragma unroll
-            for (int c = 0; c < KC; c += 2) {
-              const float2 x = make_float2(sv[c], sv[c + 1]);
-              float2 y = cap_pair_far(x, p.cap2, twice_inv);
-              if (large) {
-                float w = 0.f;
-                const float2 n = cap_pair_near(x, near, w);
-                if (x.x * x.x <= near.w_near) y.x = n.x;
-                if (x.y * x.y <= near.w_near) y.y = n.y;
-              }
-              sv[c] = y.x;
-              sv[c + 1] = y.y;
-            }
-          }
-        }
-        if (ok && p.slopes) {
-          if (__all_sync(0xffffffffu, h0 + KC - 1 <= org)) {
-            // every key at or before the origin: slope (t - org), its tile-wide part kept apart
-            shift = slope2 * static_cast<float>(h0 - org);
-#pragma unroll
-            for (int c = 0; c < KC; ++c) sv[c] = fmaf(slope2, static_cast<float>(c), sv[c]);
-          } else {
-            const float d0 = static_cast<float>(org - h0);
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-              sv[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
-          }
-        }
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < KC; ++c) sv[c] = (unseen[c / 32] >> (c % 32)) & 1u ? sv[c] : -INFINITY;
-        }
+          for (int c = 0; c < KC; c += 16)
+            tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+          tmem_wait_ld();
+        });
         if (!whole) {   // uniform over the softmax warps
           uint32_t* cm = colm + s * 16;
 #pragma unroll
           for (int k = 0; k < KC / 32; ++k) {
-            const uint32_t w = __reduce_or_sync(0xffffffffu, unseen[k]);
+            const uint32_t w = __reduce_or_sync(0xffffffffu, seen[k]);
             if (lane == 0) cm[quarter * 4 + hf * (KC / 32) + k] = w;
           }
           named_bar_sync(1, 32 * NSW);
 #pragma unroll
           for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) unseen[k] = 0;
         }
       }
       const bool full_tile = MOD || __all_sync(0xffffffffu, lim >= KT - 1);   // below the diagonal
@@ -564,9 +585,9 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
           m4[3] = max3f(m4[3], sv[c + 6], sv[c + 7]);
         }
         mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-        if constexpr (MOD) {
+        if constexpr (MOD) mx += shift;
+        if constexpr (HALVES > 1) {
           // the row's largest: this half's and the other's
-          mx += shift;
           float* hm = half_max + (L::HB > 1 ? s * 256 : 0);
           if (L::HB == 1) named_bar_sync(2, 32 * NSW);   // the last tile's have been read
           hm[hf * 128 + r] = mx;
@@ -652,17 +673,7 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
       if (MOD && (unseen[0] | unseen[1] | unseen[2] | unseen[3])) {
         // keys that no row sees (among them tokens past the end and rejected pages): the same
         ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
-        uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
-        for (int idx = threadIdx.x - 64; idx < KT * NG * 8; idx += 32 * NSW) {
-          const int tok = idx / (NG * 8);
-          const uint32_t w = tok < 64 ? (tok < 32 ? unseen[0] : unseen[1])
-                                      : (tok < 96 ? unseen[2] : unseen[3]);
-          if (!((w >> (tok & 31)) & 1u)) continue;
-          const int rem = idx % (NG * 8);
-          const int g = rem >> 3, ch = rem & 7;
-          *reinterpret_cast<uint4*>(vst + (g * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
-                                    (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-        }
+        zero_values(j, unseen, threadIdx.x - 64, 32 * NSW);
       }
       if (!MOD && j * KT + KT > Lb) {
         // tokens past the end of the request: zero their value rows so that whatever the
@@ -686,11 +697,10 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
     }
     const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag, p.dev_err));
     tc_fence_after();
-    if constexpr (MOD) {   // the halves' sums (every thread is done with its last tile)
-      float* hm = half_max;
-      hm[hf * 128 + r] = l_run;
+    if constexpr (HALVES > 1) {   // the halves' sums (every thread is done with its last tile)
+      half_max[hf * 128 + r] = l_run;
       named_bar_sync(2, 32 * NSW);
-      l_run += hm[(hf ^ 1) * 128 + r];
+      l_run += half_max[(hf ^ 1) * 128 + r];
     }
     const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
     if constexpr (RECON) {
@@ -816,7 +826,7 @@ __global__ void __launch_bounds__(pf_threads<MOD>(), 1)
       }
     }
     cluster_sync_all();
-    for (int idx = threadIdx.x; idx < RPC * D / 2; idx += pf_threads<MOD>()) {
+    for (int idx = threadIdx.x; idx < RPC * D / 2; idx += W::THREADS) {
       const int rr = idx / (D / 2), d2 = (idx % (D / 2)) * 2;
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
@@ -859,7 +869,7 @@ cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const
   const int NQ = recon ? 1 : PrefillCfg<S>::NQ;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(max_tiles * S::H * NQ);
-  cfg.blockDim = dim3(p.mod ? pf_threads<true>() : pf_threads<false>());
+  cfg.blockDim = dim3(p.mod ? PfWarps<true>::THREADS : PfWarps<false>::THREADS);
   cfg.dynamicSmemBytes = p.mod ? (recon ? PfSmem<S, true, true>::ALLOC : PfSmem<S, false, true>::ALLOC)
                                : (recon ? PfSmem<S, true>::ALLOC : PfSmem<S, false>::ALLOC);
   cfg.stream = stream;

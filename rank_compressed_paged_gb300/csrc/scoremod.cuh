@@ -3,6 +3,7 @@
 #pragma once
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "shape.h"
 
 namespace rcp {
@@ -98,10 +99,8 @@ __device__ __forceinline__ float2 cap_pair_near(float2 x, const CapNear& k, floa
   return fma_f32x2(mul_f32x2(x, w), q, x);
 }
 // Any score: 1 - 2 / (e^2u + 1), absolute error about 3e-7 of the cap as well (the two
-// approximate instructions' 2^-22 and 2^-23).  Under a cap so large that this is more than a
-// score's own rounding matters (cap2 > 128: beyond 4e-5) scores up to 0.7 of it take the
-// polynomial.
-constexpr float kCapLarge = 128.f;
+// approximate instructions' 2^-22 and 2^-23): at the largest cap allowed, 1024, 3e-4 of a unit
+// for a row with scores beyond 716, less than the rounding of its weights to fp16.
 __device__ __forceinline__ float2 cap_pair_far(float2 x, float cap2, float twice_inv) {
   const float2 a = mul_f32x2(x, both(twice_inv));   // twice_inv = 2 log2(e) / cap2
   const float2 e = add_f32x2(make_float2(fast_exp2(a.x), fast_exp2(a.y)), both(1.f));
@@ -114,6 +113,86 @@ __device__ __forceinline__ uint32_t column_bits(int32_t a, int32_t b, int32_t c0
   const uint32_t up = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
   const uint32_t dn = lo >= 32 ? 0xFFFFFFFFu : lo <= 0 ? 0u : (1u << lo) - 1u;
   return up & ~dn;
+}
+
+// A prefill row's modifications: what it sees, where its bias starts from (log2 units per
+// token), and whether one of its warp's scores has passed the range of the cap's polynomial.
+struct RowMod {
+  RowView view;
+  int32_t pos, org;
+  float slope2;
+  bool far;
+  CapNear near;
+  __device__ __forceinline__ RowMod(const AttnParams& p, int head, bool row_ok, int64_t row,
+                                    int32_t pos_, int32_t pfx)
+      : view{pfx, row_ok ? view_begin(p, row, pos_) : 0}, pos(pos_), org(bias_origin(view, pos_)),
+        slope2(p.slopes ? p.slopes[head] * 1.44269504f : 0.f), far(false),
+        near(p.cap2, p.inv_cap2) {}
+  // the 32 keys from t0 on that the row sees, without the rejected pages (two bits of bad)
+  __device__ __forceinline__ uint32_t seen(int32_t t0, uint32_t bad) const {
+    uint32_t w = column_bits(0, view.pfx, t0) | column_bits(view.lo, pos + 1, t0);
+    if (bad & 1u) w &= 0xFFFF0000u;
+    if (bad & 2u) w &= 0x0000FFFFu;
+    return w;
+  }
+};
+
+// Cap and bias of a row's scores of the keys h0 .. h0 + KC - 1, and -inf for those it does not
+// see (edge: seen[] says which; else it sees them all).  reload() reads the scores again.
+// Returns what has to be added to every score.
+template <int KC, class Reload>
+__device__ __forceinline__ float modify_scores(float (&sv)[KC], const AttnParams& p, RowMod& rm,
+                                               int32_t h0, bool edge,
+                                               const uint32_t (&seen)[KC / 32], Reload reload) {
+  float shift = 0.f;
+  if (p.cap2 > 0.f) {
+    if (!rm.far) {
+      // which form the cap takes must not depend on what hidden slots hold
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < KC; ++c) sv[c] = (seen[c / 32] >> (c % 32)) & 1u ? sv[c] : 0.f;
+      }
+      float wmax = 0.f;
+#pragma unroll
+      for (int c = 0; c < KC; c += 2) {
+        const float2 y = cap_pair_near(make_float2(sv[c], sv[c + 1]), rm.near, wmax);
+        sv[c] = y.x;
+        sv[c + 1] = y.y;
+      }
+      if (__any_sync(0xffffffffu, !(wmax <= rm.near.w_near))) {
+        // some score is past the polynomial's range; the warp stays with the general form
+        rm.far = true;
+        reload();
+      }
+    }
+    if (rm.far) {
+      const float twice_inv = 2.88539008f * p.inv_cap2;
+#pragma unroll
+      for (int c = 0; c < KC; c += 2) {
+        const float2 y = cap_pair_far(make_float2(sv[c], sv[c + 1]), p.cap2, twice_inv);
+        sv[c] = y.x;
+        sv[c + 1] = y.y;
+      }
+    }
+  }
+  if (p.slopes) {
+    if (__all_sync(0xffffffffu, h0 + KC - 1 <= rm.org)) {
+      // every key at or before the origin: slope (t - org), the part they share kept apart
+      shift = rm.slope2 * static_cast<float>(h0 - rm.org);
+#pragma unroll
+      for (int c = 0; c < KC; ++c) sv[c] = fmaf(rm.slope2, static_cast<float>(c), sv[c]);
+    } else {
+      const float d0 = static_cast<float>(rm.org - h0);
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
+        sv[c] = fmaf(-rm.slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
+    }
+  }
+  if (edge) {
+#pragma unroll
+    for (int c = 0; c < KC; ++c) sv[c] = (seen[c / 32] >> (c % 32)) & 1u ? sv[c] : -INFINITY;
+  }
+  return shift;
 }
 
 }  // namespace rcp

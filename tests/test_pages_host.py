@@ -140,7 +140,7 @@ def test_score_mod_host_checks(lib, handle):
                                      0x6000, 8, recon, p, 0x7000, 0x100000, ws, None)
         return d, f
     A = _lib.ScoreModArgs
-    for cap in (-1.0, float("nan"), INF, 2.0 ** -11, 2.0 ** 16 * 1.01):
+    for cap in (-1.0, float("nan"), INF, 2.0 ** -11, 2.0 ** 10 * 1.01):
         assert both(A(softcap=cap)) == (INV, INV), cap
     assert both(A(window=-1)) == (INV, INV)
     assert both(A(alibi_slopes=0x1002)) == (INV, INV)
@@ -148,7 +148,7 @@ def test_score_mod_host_checks(lib, handle):
     assert both(A(row_begin=0x1003)) == (INV, INV)
     assert both(A(softcap=1.0), mb=(1 << 26) + 1) == (INV, INV)
     # what is in range goes on to the checks of the plain calls
-    for mod in (None, A(), A(softcap=2.0 ** -10, window=2 ** 31 - 1), A(softcap=2.0 ** 16)):
+    for mod in (None, A(), A(softcap=2.0 ** -10, window=2 ** 31 - 1), A(softcap=2.0 ** 10)):
         assert both(mod, ws=1024) == (_lib.RCP_ERR_WORKSPACE,) * 2
     assert both(A(softcap=1.0), T=-1) == (INV, INV)
     assert both(A(softcap=1.0), recon=2)[1] == INV
