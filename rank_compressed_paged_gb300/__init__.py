@@ -145,8 +145,9 @@ def _ids(ids):
 
 def _stream(stream=None) -> int:
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def int4_page_bytes(num_heads: int, rank_k: int, rank_v: int):
@@ -241,6 +242,7 @@ class PagedCoeffCache:
         self.v_pages = v_pages
         self.dev_error = torch.zeros(1, dtype=torch.int32, device=dev)
         self._ws = None
+        self._ws_bytes = {}
         self._cfg = _lib.CacheConfig(num_heads, head_dim, rank_k, rank_v, BLOCK_SIZE,
                                      self.num_blocks, fmt)
         h = ctypes.c_void_p()
@@ -320,10 +322,15 @@ class PagedCoeffCache:
 
     # ------------------------------------------------------------------ workspace
     def workspace_bytes(self, rows: int) -> int:
-        n = ctypes.c_size_t()
-        _lib.check("rcp_workspace_size",
-                   self._lib.rcp_workspace_size(self._h, rows, ctypes.byref(n)))
-        return n.value
+        need = self._ws_bytes.get(rows)   # a function of the cache's shape alone
+        if need is None:
+            n = ctypes.c_size_t()
+            _lib.check("rcp_workspace_size",
+                       self._lib.rcp_workspace_size(self._h, rows, ctypes.byref(n)))
+            need = n.value
+            if len(self._ws_bytes) < 4096:
+                self._ws_bytes[rows] = need
+        return need
 
     def workspace(self, rows: int, need: int | None = None):
         import torch
