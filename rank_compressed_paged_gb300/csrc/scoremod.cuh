@@ -34,11 +34,6 @@ __device__ __forceinline__ int32_t bias_origin(RowView v, int32_t pos) {
   return (v.lo <= pos || pos < v.pfx) ? pos : v.pfx - 1;
 }
 
-// cap2 tanh(x / cap2), x and cap2 in log2 units
-__device__ __forceinline__ float cap_score(float x, float cap2, float inv_cap2) {
-  return cap2 * tanhf(x * inv_cap2);
-}
-
 // A prefill request's key tiles (KT keys) that some of its rows sees: those of the prefix and
 // those from the least first token of any row on, from the plan's (prefix, least first token).
 // Their pages, one after another, are the rows of V^ (reconstructing variant) and the pages
@@ -99,8 +94,13 @@ __device__ __forceinline__ float2 cap_pair_near(float2 x, const CapNear& k, floa
   return fma_f32x2(mul_f32x2(x, w), q, x);
 }
 // Any score: 1 - 2 / (e^2u + 1), absolute error about 3e-7 of the cap as well (the two
-// approximate instructions' 2^-22 and 2^-23): at the largest cap allowed, 1024, 3e-4 of a unit
-// for a row with scores beyond 716, less than the rounding of its weights to fp16.
+// approximate instructions' 2^-22 and 2^-23): at the largest cap allowed, 1024, 3e-4 of a unit,
+// less than the rounding of its weights to fp16.  The decode, which has few scores per lane and
+// page, takes it for all (a call of tanhf cost 17 % of the E4M3 step at 64 x 8192).
+__device__ __forceinline__ float cap_score(float x, float cap2, float inv_cap2) {
+  const float e = fast_exp2(x * (2.88539008f * inv_cap2));
+  return fmaf(-2.f * cap2, fast_rcp(e + 1.f), cap2);
+}
 __device__ __forceinline__ float2 cap_pair_far(float2 x, float cap2, float twice_inv) {
   const float2 a = mul_f32x2(x, both(twice_inv));   // twice_inv = 2 log2(e) / cap2
   const float2 e = add_f32x2(make_float2(fast_exp2(a.x), fast_exp2(a.y)), both(1.f));

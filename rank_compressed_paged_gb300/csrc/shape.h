@@ -170,7 +170,8 @@ struct AttnParams {
   // workspace regions
   int64_t* cum;               // [nq+1] prefix sums of blocks per query row (decode: written
                               // by partition 0 of the split-K kernel for the combine)
-  int32_t* qlen;              // [nq] keys attended by each query row (prefill plan)
+  int32_t* qlen;              // [nq] keys attended by each query row (prefill plan); decode with
+                              // score modifications: pages read for each request
   int32_t* qrow;              // [nq] block-table row of each query row (prefill plan)
   float* qt;                  // [nq][H][r_k] rank-space queries, scaled by log2(e)/sqrt(d)
   float* rec;                 // [(nq + parts)][REC] split partials
