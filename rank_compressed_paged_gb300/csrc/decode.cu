@@ -51,6 +51,29 @@ namespace rcp {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanRegRows = 16;
 
+// Least first token behind the prefix of a chunk's n rows, at positions pos0 .. (a warp; every
+// lane gets it), INT32_MAX if no row sees one.
+__device__ __forceinline__ int32_t plan_first_token(const AttnParams& p, int32_t c0, int32_t n,
+                                                    int32_t pos0, int lane) {
+  int32_t lo = INT32_MAX;
+  if (p.row_begin == nullptr) {   // a window alone: the first row's
+    if (n > 0) lo = view_begin(p, c0, pos0);
+  } else {
+    for (int32_t i0 = lane; i0 < n; i0 += 32 * kPlanRegRows) {   // loads in flight together
+      int32_t f[kPlanRegRows];
+#pragma unroll
+      for (int k = 0; k < kPlanRegRows; ++k) {
+        const int32_t i = i0 + 32 * k;
+        f[k] = i < n ? view_begin(p, c0 + i, pos0 + i) : INT32_MAX;
+      }
+#pragma unroll
+      for (int k = 0; k < kPlanRegRows; ++k)
+        if (f[k] <= pos0 + i0 + 32 * k) lo = min(lo, f[k]);
+    }
+  }
+  return __reduce_min_sync(0xffffffffu, lo);
+}
+
 // One CTA: keys attended (qlen) and block-table row (qrow) of every chunk row, the prefix
 // sums of their blocks, the list of 128-row query tiles and (reconstructing variant) the
 // page prefix sums of the requests with chunk rows.  Launched as a programmatic dependent
@@ -66,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
     const int tid = threadIdx.x;
     const int32_t max_len = p.bt_stride * kBlockSize;
     if (tid == 0) cu_bad = 0;
-    for (int r = tid; r < p.nq; r += kPlanThreads) {
+    for (int r = tid; r < p.nq && !p.mod; r += kPlanThreads) {
       p.qlen[r] = 0;
       p.qrow[r] = 0;
     }
@@ -96,30 +119,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
           if ((tid & 31) == 0) atomicOr(p.dev_err, RCP_DEVERR_BAD_LEN);
           continue;
         }
+        if (p.mod) {
+          // score modifications: no row lists (the prefill kernels read none), but the prefix
+          // and, for the variants that gather pages, the least first token of the rows
+          if (p.vmap != nullptr) {
+            const int32_t lo = plan_first_token(p, c0, n, L - n, tid & 31);
+            if ((tid & 31) == 0) {
+              p.vmap[2 * b] = view_prefix(p, b, L);
+              p.vmap[2 * b + 1] = lo;
+            }
+          }
+          continue;
+        }
         for (int32_t i = tid & 31; i < n; i += 32) {
           p.qlen[c0 + i] = L - n + i + 1;   // causal: row i sees keys 0 .. P + i
           p.qrow[c0 + i] = b;
-        }
-        if (p.vmap != nullptr) {
-          // score modifications: the prefix and the least first token of the request's rows
-          int32_t lo = INT32_MAX;   // none sees a token behind the prefix
-          for (int32_t i = tid & 31; i < n; i += 32) {
-            const int32_t pos = L - n + i, f = view_begin(p, c0 + i, pos);
-            if (f <= pos && f < lo) lo = f;
-          }
-          lo = __reduce_min_sync(0xffffffffu, lo);
-          if ((tid & 31) == 0) {
-            p.vmap[2 * b] = view_prefix(p, b, L);
-            p.vmap[2 * b + 1] = lo;
-          }
         }
       }
     }
     __syncthreads();
     // block-wide exclusive scan of per-thread sums (contiguous row ranges per thread); a
     // thread's lengths are loaded kPlanRegRows at a time, all loads in flight together
-    const int per = (p.nq + kPlanThreads - 1) / kPlanThreads;
-    const int r0 = min(p.nq, tid * per), r1 = min(p.nq, r0 + per);
+    const int nrows = p.mod ? 0 : p.nq;
+    const int per = (nrows + kPlanThreads - 1) / kPlanThreads;
+    const int r0 = min(nrows, tid * per), r1 = min(nrows, r0 + per);
     int64_t s = 0;
     for (int rb = r0; rb < r1; rb += kPlanRegRows) {
       int32_t q[kPlanRegRows];
