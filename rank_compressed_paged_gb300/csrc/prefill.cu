@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   griddep_wait();            // plan and rank-space queries are ready
-  griddep_launch();
   const int slot = blockIdx.x / (H * NQ);
   const int h = (blockIdx.x / NQ) % H;
   const int slice = blockIdx.x % NQ;                    // cluster rank when NQ > 1
@@ -195,6 +194,9 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now: the next launch's CTAs, which hold tensor memory while they wait for this one,
+  // must not take this CTA's place in it
+  griddep_launch();
   const uint32_t tmem = *tmem_slot;
   int32_t pfx = 0, lo_min = 0, lo_max = 0, npt = 0, lt = 0;   // MOD: tiles [0, npt), then lt ..
   if constexpr (MOD) {

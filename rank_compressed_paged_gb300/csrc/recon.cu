@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(kRcThreads, 1)
   const int64_t cid = blockIdx.x / CL, ncl = gridDim.x / CL;   // cluster, clusters
 
   griddep_wait();   // page prefix sums (plan) and the appended chunk are visible
-  griddep_launch();
   const int64_t total = p.vcum[p.batch];
   const int64_t ntiles = (total + 2 * BPT - 1) / (2 * BPT) * NU;   // cluster work units
   if (cid >= ntiles) return;   // uniform over the cluster, before any cluster operation
@@ -143,6 +142,9 @@ __global__ void __launch_bounds__(kRcThreads, 1)
   tc_fence_before();
   cluster_sync_all();   // every CTA's barriers exist before any copy or arrival reaches them
   tc_fence_after();
+  // only now: the next launch's CTAs, which hold tensor memory while they wait for this one,
+  // must not take this CTA's place in it
+  griddep_launch();
   const uint32_t tmem = *tmem_slot;
   auto col_tile = [&](int64_t t) { return static_cast<int>(t % NU) * P + pr; };
 
