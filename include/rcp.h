@@ -123,8 +123,9 @@ rcp_status rcp_destroy_cache(rcp_cache* cache);
  * budget).  alloc hands out n free physical ids into ids_out[0..n) (host array, caller
  * owned; RCP_ERR_CAPACITY and no change if fewer are free); free returns n ids from a
  * host array (RCP_ERR_CAPACITY and no change on an out-of-range, already-free or repeated
- * id); num_free reports the free count.  Pure host bookkeeping, no CUDA call; a handle is
- * not thread-safe. */
+ * id; a block with further references, rcp_fork_blocks, loses one and stays); num_free
+ * reports the free count.  Pure host bookkeeping, no CUDA call; a handle is not
+ * thread-safe. */
 rcp_status rcp_alloc_blocks(rcp_cache* cache, int32_t n, int32_t* ids_out);
 rcp_status rcp_free_blocks(rcp_cache* cache, int32_t n, const int32_t* ids);
 rcp_status rcp_num_free_blocks(const rcp_cache* cache, int64_t* n_free);
@@ -134,8 +135,8 @@ rcp_status rcp_num_free_blocks(const rcp_cache* cache, int64_t* n_free);
  * "Per-decode-step attention" section's split attention and its combine step (Proxima
  * page, "Kernel profiling breakdown", the combine-splits kernel), the plan and the
  * rank-space queries.  The caller allocates it (256-byte aligned) and may reuse it for
- * every call on one stream.  Pure host arithmetic; RCP_ERR_INVALID_ARG for a null
- * handle or output, or a negative row count. */
+ * every call on one stream; calls that may overlap on the GPU need one each.  Pure host
+ * arithmetic; RCP_ERR_INVALID_ARG for a null handle or output, or a negative row count. */
 rcp_status rcp_workspace_size(const rcp_cache* cache, int32_t max_query_rows, size_t* bytes);
 
 /* Append (Proxima page, "Kernel profiling breakdown": the cache-write kernel does the
@@ -270,7 +271,8 @@ rcp_status rcp_prefill_crossover_rows(const rcp_cache* cache, int32_t* rows);
  *     s = s - alibi_slopes[h] |pos - t|.
  * A row that sees no token gives zeros.  A zero or NULL member leaves its part out:
  *   softcap       cap of the scores, 0 or in [2^-10, 2^10];
- *   alibi_slopes  [H] fp32 device, finite: a bias that falls with the distance;
+ *   alibi_slopes  [H] fp32 device, of magnitude 2^60 at most: a bias that falls with the
+ *                 distance (grows, where negative);
  *   window        >= 0: the last `window` tokens up to and including the row's own;
  *   prefix_lens   [batch] int32 device: tokens that every row of the request sees, whatever
  *                 its position (a prefix mask, where rows of the prefix also see later ones of
@@ -348,8 +350,8 @@ rcp_status rcp_fork_sequence(rcp_cache* cache, const int32_t* ids, int32_t num_b
  * overlapping seq_lens.  The caller frees the pages past ceil(new_lens[b] / 16) once it has
  * read new_lens.  Device errors: a length outside the table sets RCP_DEVERR_BAD_LEN, its
  * request stays as it is and new_lens[b] = 0; a bad block id on a move's way sets
- * RCP_DEVERR_BAD_BLOCK and that token is not moved.  RCP_ERR_INVALID_ARG for null,
- * misaligned or overlapping arguments or max_blocks_per_seq above 2^26,
+ * RCP_DEVERR_BAD_BLOCK and that token is not moved.  RCP_ERR_INVALID_ARG for null or
+ * misaligned arguments, lengths that overlap or max_blocks_per_seq above 2^26,
  * RCP_ERR_UNSUPPORTED for a batch above 2^20. */
 rcp_status rcp_compact_tokens(rcp_cache* cache, const int32_t* block_table,
                               int32_t max_blocks_per_seq, const int32_t* seq_lens,

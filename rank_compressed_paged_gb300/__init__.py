@@ -140,6 +140,8 @@ def _on_current(device) -> None:
 
 
 def _ids(ids):
+    if any(not -2**31 <= i < 2**31 for i in ids):   # ctypes would keep the low 32 bits
+        raise ValueError("block ids must fit 32 bits")
     return (ctypes.c_int32 * max(len(ids), 1))(*ids)
 
 
@@ -241,7 +243,7 @@ class PagedCoeffCache:
         self.k_pages = k_pages
         self.v_pages = v_pages
         self.dev_error = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._ws = None
+        self._ws = {}         # by stream
         self._ws_bytes = {}
         self._cfg = _lib.CacheConfig(num_heads, head_dim, rank_k, rank_v, BLOCK_SIZE,
                                      self.num_blocks, fmt)
@@ -265,8 +267,7 @@ class PagedCoeffCache:
         return [ids[i] for i in range(n)]
 
     def free_blocks(self, ids) -> None:
-        arr = (ctypes.c_int32 * max(len(ids), 1))(*ids)
-        _lib.check("rcp_free_blocks", self._lib.rcp_free_blocks(self._h, len(ids), arr))
+        _lib.check("rcp_free_blocks", self._lib.rcp_free_blocks(self._h, len(ids), _ids(ids)))
 
     def num_free_blocks(self) -> int:
         n = ctypes.c_int64()
@@ -290,6 +291,8 @@ class PagedCoeffCache:
         of block ids, each sharing the full pages and holding a copy of the last, partly
         filled one (queued on the stream)."""
         _on_current(self.device)
+        if not 0 <= length <= len(ids) * BLOCK_SIZE or not 0 <= children < 2**31:
+            raise ValueError(f"{len(ids)} blocks hold no {length} tokens for {children} children")
         n = -(-int(length) // BLOCK_SIZE)
         out = (ctypes.c_int32 * max(n * int(children), 1))()
         _lib.check("rcp_fork_sequence", self._lib.rcp_fork_sequence(
@@ -332,12 +335,22 @@ class PagedCoeffCache:
                 self._ws_bytes[rows] = need
         return need
 
-    def workspace(self, rows: int, need: int | None = None):
+    def workspace(self, rows: int, need: int | None = None, stream=None):
+        """Scratch for a call of ``rows`` query rows (or of ``need`` bytes) on ``stream``, reused
+        by the stream's later calls.  Calls on two streams may overlap and get one each; a call
+        that is captured gets one from its graph's memory, which no other graph or call uses."""
         import torch
+        if stream is not None and stream != torch.cuda.current_stream():
+            with torch.cuda.stream(stream):
+                return self.workspace(rows, need)
         need = self.workspace_bytes(rows) if need is None else need
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_pages.device)
-        return self._ws
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        key = _stream()
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < need:
+            ws = self._ws[key] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return ws
 
     def reconstruct_workspace_bytes(self, rows: int, batch: int, max_blocks_per_seq: int) -> int:
         n = ctypes.c_size_t()
@@ -398,7 +411,7 @@ class PagedCoeffCache:
             out = torch.empty_like(q)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
-        ws = self.workspace(B) if workspace is None else workspace
+        ws = self.workspace(B, stream=stream) if workspace is None else workspace
         _validate_workspace(self.device, ws)
         if mod is not None:
             self._decode_mod(mod, None, q, block_table, seq_lens, out, ws, stream)
@@ -421,7 +434,7 @@ class PagedCoeffCache:
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
         if page_kept is not None:
             _need("page_kept", page_kept, torch.uint8, tuple(block_table.shape), self.device)
-        ws = self.workspace(B) if workspace is None else workspace
+        ws = self.workspace(B, stream=stream) if workspace is None else workspace
         _validate_workspace(self.device, ws)
         _lib.check("rcp_decode_attn_sparse", self._lib.rcp_decode_attn_sparse(
             self._h, _ptr(q), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), B,
@@ -438,7 +451,7 @@ class PagedCoeffCache:
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         _validate_append(self.device, H, d, k, v, slot_mapping)
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
-        ws = self.workspace(B) if workspace is None else workspace
+        ws = self.workspace(B, stream=stream) if workspace is None else workspace
         _validate_workspace(self.device, ws)
         if mod is not None:
             self._decode_mod(mod, (k, v, slot_mapping), q, block_table, seq_lens, out, ws, stream)
@@ -463,11 +476,11 @@ class PagedCoeffCache:
             raise ValueError(f"unknown prefill variant {variant!r}")
         return variant
 
-    def _prefill_workspace(self, variant: str, rows: int, B: int, mb: int):
+    def _prefill_workspace(self, variant: str, rows: int, B: int, mb: int, stream):
         # quantized pages are widened into the workspace first (both variants)
         if variant == "rank" and self.page_format == "fp16":
-            return self.workspace(rows, self.workspace_bytes(rows))
-        return self.workspace(rows, self.reconstruct_workspace_bytes(rows, B, mb))
+            return self.workspace(rows, stream=stream)
+        return self.workspace(rows, self.reconstruct_workspace_bytes(rows, B, mb), stream)
 
     def _prefill_mod(self, mod, app, q, cu_chunk_lens, block_table, seq_lens, out, ws, stream,
                      variant: str):
@@ -502,7 +515,8 @@ class PagedCoeffCache:
                                     out)
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B, mod)
-        ws = self._prefill_workspace(variant, rows, B, mb) if workspace is None else workspace
+        ws = (self._prefill_workspace(variant, rows, B, mb, stream) if workspace is None
+              else workspace)
         if mod is not None:
             _validate_workspace(self.device, ws)
             self._prefill_mod(mod, None, q, cu_chunk_lens, block_table, seq_lens, out, ws, stream,
@@ -532,7 +546,8 @@ class PagedCoeffCache:
                                     out)
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B, mod)
-        ws = self._prefill_workspace(variant, rows, B, mb) if workspace is None else workspace
+        ws = (self._prefill_workspace(variant, rows, B, mb, stream) if workspace is None
+              else workspace)
         _validate_workspace(self.device, ws)
         if mod is not None:
             self._prefill_mod(mod, (k, v, slot_mapping), q, cu_chunk_lens, block_table, seq_lens,

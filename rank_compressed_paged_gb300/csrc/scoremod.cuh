@@ -127,7 +127,9 @@ struct RowMod {
                                     int32_t pos_, int32_t pfx)
       : view{pfx, row_ok ? view_begin(p, row, pos_) : 0}, pos(pos_), org(bias_origin(view, pos_)),
         slope2(p.slopes ? p.slopes[head] * 1.44269504f : 0.f), far(false),
-        near(p.cap2, p.inv_cap2) {}
+        near(p.cap2, p.inv_cap2) {
+    if (!row_ok) near.w_near = INFINITY;   // a row outside the chunk has no say in the form
+  }
   // the 32 keys from t0 on that the row sees, without the rejected pages (two bits of bad)
   __device__ __forceinline__ uint32_t seen(int32_t t0, uint32_t bad) const {
     uint32_t w = column_bits(0, view.pfx, t0) | column_bits(view.lo, pos + 1, t0);

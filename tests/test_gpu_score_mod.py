@@ -455,3 +455,165 @@ def test_prefill_step_appends_first_and_replays_on_a_side_stream(variant):
     torch.cuda.synchronize()
     assert cache.read_device_error() == 0
     assert torch.equal(eager, out)
+
+
+# ------------------------------------------------------------- biases, padding, streams, graphs
+def odd_slopes(shape):
+    """Biases that grow with the distance, steep ones and none.  A prefill tile's terms reach
+    128 * 4 log2(e) < 2^10, of which fp32 keeps 2^-14 / 2: within the bound's 2^-15 of a unit
+    (times log 2)."""
+    return [(-0.05, 4.0, 0.0, -0.4, 0.3)[h % 5] for h in range(shape["num_heads"])]
+
+
+@pytest.mark.parametrize("extra", [dict(), dict(window=90, prefix_lens=7, softcap=11.0)])
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("main", "fp8_e4m3"), ("tiny", "int4")])
+def test_biases_of_either_sign(shape_name, pages, extra):
+    import torch
+    for chunked in (False, True):
+        inp = prefill_inputs(shape_name, pages) if chunked else decode_inputs(shape_name, pages)
+        mod = dict(alibi_slopes=odd_slopes(inp.shape), **extra)
+        if "prefix_lens" in mod:
+            mod["prefix_lens"] = np.full(len(PRIOR if chunked else LENS), mod["prefix_lens"])
+        if chunked:
+            ref = oracle_prefill(inp, shape_name, pages, f"odd{len(extra)}", mod)
+            for variant in ("rank", "reconstruct"):
+                cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+                out = cache.prefill_attn(t(inp.q), t(inp.cu_chunk_lens), t(inp.cache.block_table),
+                                         t(inp.seq_lens_after), variant=variant, mod=score_mod(mod))
+                assert_within(out.cpu().numpy(), ref, f"prefill {variant}")
+        else:
+            cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+            out = cache.decode_attn(t(inp.q), t(inp.cache.block_table), t(inp.cache.seq_lens),
+                                    mod=score_mod(mod))
+            assert_within(out.cpu().numpy(), oracle_decode(inp, pages, mod), "decode")
+        torch.cuda.synchronize()
+        assert cache.read_device_error() == 0
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("tiny", "fp8_e4m3")])
+def test_prefill_rows_outside_the_chunks_are_left_as_they_were(shape_name, pages, variant):
+    """Query rows ahead of the first chunk and behind the last one (a padded batch), whose
+    row_begin holds anything."""
+    import torch
+    inp = prefill_inputs(shape_name, pages)
+    rows, ahead, behind = sum(CHUNK), 3, 140
+    begin = doc_begin(rows, PRIOR, CHUNK, 50)
+    mod = dict(softcap=6.0, row_begin=begin)
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    args = (t(inp.cache.block_table), t(inp.seq_lens_after))
+    pad = [(ahead, behind), (0, 0), (0, 0)]
+    q = np.pad(inp.q, pad, constant_values=np.nan)
+    cu = (np.asarray(inp.cu_chunk_lens) + ahead).astype(np.int32)
+    wide = np.concatenate([[-5, 2 ** 31 - 1, -2 ** 31], begin, np.full(behind, -2 ** 31)])
+    out = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda")
+    cache.prefill_attn(t(q), t(cu), *args, out=out, variant=variant,
+                       mod=score_mod(dict(mod, row_begin=wide)))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert bool((out[:ahead] == 7.0).all()) and bool((out[ahead + rows:] == 7.0).all())
+    assert_within(out[ahead:ahead + rows].cpu().numpy(),
+                  oracle_prefill(inp, shape_name, pages, "padded", mod), f"{shape_name} {variant}")
+
+
+def stream_jobs(cache, shape, n):
+    """Decodes and prefills of several masks over one cache: (call(stream, out), output)."""
+    import torch
+    rng = np.random.default_rng(331)
+    jobs = []
+    for i in range(n):
+        B = 3 + 5 * i
+        lens = rng.integers(1, 700, B).astype(np.int32)
+        table = rng.integers(0, cache.num_blocks, (B, 44)).astype(np.int32)
+        table, lens = t(table), t(lens)
+        H, d = shape["num_heads"], shape["head_dim"]
+        if i % 2 == 0:
+            q = t(wl.fp16(rng.standard_normal((B, H, d)) * 3))
+            mod = score_mod(dict(softcap=4.0 + i, window=200, prefix_lens=np.full(B, 20)))
+
+            def call(stream, out, a=(q, table, lens), mod=mod):
+                cache.decode_attn(*a, out=out, stream=stream, mod=mod)
+        else:
+            chunk = np.minimum(lens.cpu().numpy(), 1 + 40 * i)
+            cu = t(np.concatenate([[0], np.cumsum(chunk)]).astype(np.int32))
+            q = t(wl.fp16(rng.standard_normal((int(chunk.sum()), H, d)) * 3))
+            mod = score_mod(dict(softcap=9.0, alibi_slopes=slopes_of(shape), window=150 + i))
+
+            def call(stream, out, a=(q, cu, table, lens), mod=mod):
+                cache.prefill_attn(*a, out=out, stream=stream, mod=mod)
+        jobs.append((call, torch.empty_like(q)))
+    return jobs
+
+
+def stream_cache(shape_name, pages):
+    shape = SHAPES[shape_name]
+    rng = np.random.default_rng(332)
+    H, d, rk, R = (shape[k] for k in ("num_heads", "head_dim", "rank_k", "rank_v"))
+    k = wl.fp16(rng.standard_normal((300, H, 16, rk)))
+    v = wl.fp16(rng.standard_normal((300, 16, R)))
+    U = wl.fp16(rng.standard_normal((H, rk, d)) / np.sqrt(rk))
+    W = wl.fp16(rng.standard_normal((R, H * d)) / np.sqrt(R))
+    return shape, cache_of(pages, shape, U, W, *encode(pages, k, v))
+
+
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("main", "fp8_e4m3"), ("tiny", "int4")])
+def test_calls_on_several_streams_at_once(shape_name, pages):
+    """Calls that overlap, each on a stream of its own with the cache's own workspaces."""
+    import torch
+    shape, cache = stream_cache(shape_name, pages)
+    jobs = stream_jobs(cache, shape, 4)
+    want = []
+    for call, out in jobs:
+        call(None, out)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(10):
+        for _, out in jobs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, (call, out) in zip(streams, jobs):
+                call(s, out)
+        torch.cuda.synchronize()
+        for (_, out), w in zip(jobs, want):
+            assert torch.equal(out, w)
+    assert cache.read_device_error() == 0
+
+
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("tiny", "int4")])
+def test_captured_calls_keep_their_workspaces(shape_name, pages):
+    """Graphs captured without a workspace of the caller's: replayed after larger eager calls
+    have replaced the cache's, and both at once."""
+    import torch
+    shape, cache = stream_cache(shape_name, pages)
+    jobs = stream_jobs(cache, shape, 4)
+    want = []
+    for call, out in jobs[:2]:
+        call(None, out)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    graphs = []
+    for call, out in jobs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(None, out)
+        graphs.append(g)
+    for call, out in jobs[2:]:                           # larger workspaces
+        call(None, out)
+    torch.cuda.synchronize()
+    junk = [torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(10):
+        for _, out in jobs[:2]:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(jobs, want):
+            assert torch.equal(out, w)
+    assert cache.read_device_error() == 0
+    assert all(bool((x == 255).all()) for x in junk)     # nothing wrote to memory handed on
