@@ -500,7 +500,7 @@ rcp_status run_attention(rcp_cache* c, const void* q, const int32_t* cu_chunk, i
         e = rcp::launch_recon<ShapeMain>(vsrc, c->tmap_wv_mn, p, max_pages, c->num_sms, s, pdl);
       if (e == cudaSuccess)
         e = rcp::launch_prefill<ShapeMain>(qhi_map, qlo_map, kmap, vals, c->tmap_wv_mn, p,
-                                           max_tiles, s, pdl, recon);
+                                           max_tiles, c->num_sms, s, pdl, recon);
     } else {
       e = rcp::launch_plan<ShapeTiny>(p, s, pdl);
       if (e == cudaSuccess && fused) {
@@ -519,7 +519,7 @@ rcp_status run_attention(rcp_cache* c, const void* q, const int32_t* cu_chunk, i
         e = rcp::launch_recon<ShapeTiny>(vsrc, c->tmap_wv_mn, p, max_pages, c->num_sms, s, pdl);
       if (e == cudaSuccess)
         e = rcp::launch_prefill<ShapeTiny>(qhi_map, qlo_map, kmap, vals, c->tmap_wv_mn, p,
-                                           max_tiles, s, pdl, recon);
+                                           max_tiles, c->num_sms, s, pdl, recon);
     }
     if (e == cudaSuccess && c->prof_stop) e = cudaEventRecord(c->prof_stop, s);
     return e == cudaSuccess ? RCP_OK : RCP_ERR_CUDA;

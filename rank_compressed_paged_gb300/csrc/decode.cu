@@ -211,7 +211,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
         }
         t0 += nt;
       }
-      if (tid == kPlanThreads - 1) *p.tcount = static_cast<int32_t>(t0);
+      if (tid == kPlanThreads - 1) {
+        p.tcount[0] = static_cast<int32_t>(t0);
+        p.tcount[1] = 0;
+      }
       if (p.vcum != nullptr) {
         // reconstructing prefill: pages of every request with chunk rows, in request
         // order (the rows of V^)

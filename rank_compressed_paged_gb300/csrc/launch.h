@@ -24,7 +24,7 @@ cudaError_t prepare_prefill();
 template <class S>
 cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const CUtensorMap& kp,
                            const CUtensorMap& vp, const CUtensorMap& w, const AttnParams& p,
-                           int max_tiles, cudaStream_t stream, bool pdl, bool recon);
+                           int max_tiles, int num_sms, cudaStream_t stream, bool pdl, bool recon);
 // V^ = C_v W_v for the pages of every request with chunk rows (max_pages bounds them), by
 // persistent CTA pairs (at most num_sms / 2).
 template <class S>

@@ -32,13 +32,14 @@
 // keys of a tile each, because one warp per scheduler cannot hide the arithmetic added to every
 // score (16 x (4096 + 256), cap + bias: 1071 -> 914 us); the value copies are warp 10's.  The
 // key tiles are those that some row of the CTA sees, the nearest first.  Measured per tile
-// (cycles): 2500 with masks alone, 3630 with a cap (FMA pipe), plain 2210; whole calls 0.88 ms
+// (cycles): 2500 with masks alone, 3600 with a cap (FMA pipe), plain 2210; whole calls 0.87 ms
 // with cap and bias and 0.76 ms with masks, plain 0.70 ms.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "launch.h"
 #include "ptx.cuh"
@@ -60,7 +61,7 @@ constexpr float kPfRescale = 8.f;   // log2 units: weights stay below 2^8 betwee
 
 // RECON: the values are the reconstructed V^ rows of head h (N = d) instead of a slice
 // of the joint coefficients (N = RQ), and the epilogue writes O directly.
-template <class S, bool RECON, bool MOD = false>
+template <class S, bool RECON, bool MOD = false, bool PERS = false>
 struct PfSmem {
   using C = PrefillCfg<S>;
   static constexpr int VN = RECON ? S::D : C::RQ;       // value MMA N
@@ -75,7 +76,9 @@ struct PfSmem {
   // operand of the value MMA); the rank-space variant stages it in shared memory
   static constexpr int P_BYTES = RECON ? 0 : 128 * C::KT * 2;
   static constexpr int P_TM = 256 + VN;
-  static constexpr int ST_OFF = 2 * Q_BYTES;            // q~ hi at 0, q~ lo at Q_BYTES
+  static_assert(!PERS || (RECON && MOD), "variants");
+  static constexpr int QB = PERS ? 2 : 1;               // query buffers (this item, the next)
+  static constexpr int ST_OFF = QB * 2 * Q_BYTES;       // q~ hi at 0, q~ lo at Q_BYTES
   static constexpr int P_OFF = ST_OFF + NS * STAGE;
   static constexpr int ZH_OFF = ST_OFF;                 // epilogue reuses the stage memory
   static constexpr int ZL_OFF = ZH_OFF + 128 * C::RQ * 2;
@@ -83,15 +86,18 @@ struct PfSmem {
   static constexpr int W_BYTES = C::RQ * S::D * 2;
   static constexpr int END = (RECON || P_OFF + P_BYTES > W_OFF + W_BYTES) ? P_OFF + P_BYTES
                                                                              : W_OFF + W_BYTES;
-  static constexpr int NBAR = 11 + 4 * NS;
+  static constexpr int NBAR = 11 + 4 * NS + (PERS ? 7 : 0);
   static constexpr int BAR_OFF = END;                   // NBAR mbarriers
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;   // tmem slot, abort flag
   // MOD: least and largest first token of the tile's rows (per warp), the rejected pages of
   // each key stage and of each score buffer, the softmax warps' column masks [2][4][4] and the
-  // row halves' maxima [HB][2][128] (the rank-space variant has room for one buffer)
+  // row halves' maxima [HB][2][128] (the rank-space variant has room for one buffer).
+  // PERS: the row halves' sums [2][128] and two work items
   static constexpr int MOD_OFF = MISC_OFF + 16;
   static constexpr int HB = RECON ? 2 : 1;
-  static constexpr int MOD_BYTES = MOD ? (8 + 8 + 2 + 2 * 16 + HB * 2 * 128) * 4 : 0;
+  static constexpr int ITEM = 12;                       // ints of a work item
+  static constexpr int MOD_BYTES =
+      (MOD ? (8 + 8 + 2 + 2 * 16 + HB * 2 * 128) * 4 : 0) + (PERS ? (2 * 128 + 2 * ITEM) * 4 : 0);
   static constexpr int TOTAL = MOD_OFF + MOD_BYTES;
   static constexpr int ALLOC = TOTAL + 1024;
   static constexpr int RPC = 128 / NQ;                  // output rows each slice CTA sums
@@ -106,7 +112,13 @@ struct PfSmem {
 // its own lo, so the CTA walks the key tiles of the prefix and those from the least lo of
 // its rows on; each row masks its scores to what it sees, and a key that no row of the tile
 // sees has its value row zeroed.
-template <class S, bool RECON, bool MOD>
+//
+// PERS (MOD with RECON, launch_prefill's rule): one CTA per SM takes (query tile, head) items
+// until none is left, from a counter that the plan resets.  The key warp works out the next
+// item and loads its queries and first keys, and its first scores are computed, while the
+// softmax warps finish this one.  A CTA per item spends 10,000 cycles on starting and ending,
+// as much as four key tiles: packed documents of about 700 tokens, 2 x 4096, 274 -> 238 us.
+template <class S, bool RECON, bool MOD, bool PERS>
 __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qhi_map,
                    const __grid_constant__ CUtensorMap qlo_map,
@@ -115,7 +127,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
                    const __grid_constant__ CUtensorMap w_map,
                    const __grid_constant__ AttnParams p) {
   using C = PrefillCfg<S>;
-  using L = PfSmem<S, RECON, MOD>;
+  using L = PfSmem<S, RECON, MOD, PERS>;
   constexpr int KT = C::KT, RQ = C::RQ, NQ = L::NQ, NG = L::NG, VN = L::VN, D = S::D, H = S::H;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -134,28 +146,44 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
   uint64_t* zq_full = acc_done + 1;
   uint64_t* w_full = zq_full + 1;
   uint64_t* o_done = w_full + 1;
+  uint64_t* q_empty = o_done + 1;           // PERS [2] a query buffer is no longer used
+  uint64_t* item_full = q_empty + 2;        // PERS [2] a work item is written
+  uint64_t* item_empty = item_full + 2;     // PERS [2] ... and read by every warp that does
+  uint64_t* q_full2 = item_empty + 2;       // PERS: of the second query buffer
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // MOD: by a shuffle, which tells the compiler that a warp's role is uniform (16 x (4096 + 256),
+  // cap + bias: 881 -> 865 us)
+  const int warp = MOD ? __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0) : threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
 
   griddep_wait();            // plan and rank-space queries are ready
-  const int slot = blockIdx.x / (H * NQ);
-  const int h = (blockIdx.x / NQ) % H;
   const int slice = blockIdx.x % NQ;                    // cluster rank when NQ > 1
-  if (slot >= *p.tcount) return;                        // uniform over the cluster
-  const int b = p.tile_b[slot], qt = p.tile_qt[slot];
-  const int c0 = p.cu_chunk[b], n = p.cu_chunk[b + 1] - c0;
-  const int Lb = p.seq_lens[b], P0 = Lb - n;
-  const int i0 = qt * 128;                              // first chunk row of this tile
-  const int i_last = min(n, i0 + 128) - 1;
-  int nkt = (P0 + i_last + 1 + KT - 1) / KT;            // key tiles (causal limit)
-  const int nblk = (Lb + kBlockSize - 1) / kBlockSize;
-  const int row0 = c0 + i0;
+  if (!PERS && blockIdx.x / (H * NQ) >= *p.tcount) return;   // uniform over the cluster
+  // the (query tile, head) of this CTA; PERS: of the item that this warp is at
+  int h = 0, b = 0, n = 0, P0 = 0, nkt = 0, nblk = 0, i0 = 0, row0 = 0, Lb = 0;
+  auto locate = [&](int slot) {
+    b = p.tile_b[slot];
+    i0 = p.tile_qt[slot] * 128;                         // first chunk row of this tile
+    const int c0 = p.cu_chunk[b];
+    n = p.cu_chunk[b + 1] - c0;
+    Lb = p.seq_lens[b];
+    P0 = Lb - n;
+    nkt = (P0 + min(n, i0 + 128) - 1 + KT) / KT;        // key tiles (causal limit)
+    nblk = (Lb + kBlockSize - 1) / kBlockSize;
+    row0 = c0 + i0;
+  };
+  if constexpr (!PERS) {
+    h = (blockIdx.x / NQ) % H;
+    locate(blockIdx.x / (H * NQ));
+  }
   int* wlo = reinterpret_cast<int*>(sm + L::MOD_OFF);   // MOD [8]: least, largest lo per warp
   int* kbad = wlo + 8;                                  // MOD [8]: rejected pages of a tile
   int* sbad = kbad + 8;                                 // MOD [2]: the same per score buffer
   uint32_t* colm = reinterpret_cast<uint32_t*>(sbad + 2);   // MOD [2][4][4]
   float* half_max = reinterpret_cast<float*>(colm + 32);    // MOD [HB][2][128]
+  float* half_sum = half_max + (PERS ? L::HB * 256 : 0);    // MOD [2][128]
+  int* items = reinterpret_cast<int*>(half_sum + 256);      // PERS [2][ITEM]
   using W = PfWarps<MOD>;
   constexpr int NSW = W::NSW;                               // softmax warps 2 .. NSW + 1
   constexpr int HALVES = NSW / 4;                           // threads per query row
@@ -178,6 +206,14 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     mbar_init(zq_full, NSW);
     mbar_init(w_full, 1);
     mbar_init(o_done, 1);
+    if constexpr (PERS) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&q_empty[i], 1 + NSW);      // its last score MMA, the softmax warps
+        mbar_init(&item_full[i], 1);
+        mbar_init(&item_empty[i], 2 + NSW);   // the MMA, value-copy and softmax warps
+      }
+      mbar_init(q_full2, 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -186,10 +222,10 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     tmem_relinquish();
   }
   // MOD: rows of this tile by thread, their first tokens; rows past the chunk do not count
-  if constexpr (MOD) {
+  if constexpr (MOD && !PERS) {
     if (warp < 4) {
       const int ci = i0 + static_cast<int>(threadIdx.x);
-      const int32_t f = ci < n ? view_begin(p, c0 + ci, P0 + ci) : 0;
+      const int32_t f = ci < n ? view_begin(p, row0 - i0 + ci, P0 + ci) : 0;
       const int32_t least = __reduce_min_sync(0xffffffffu, ci < n && f <= P0 + ci ? f : INT32_MAX);
       const int32_t most = __reduce_max_sync(0xffffffffu, ci < n ? f : 0);
       if (lane == 0) {
@@ -206,15 +242,42 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
   griddep_launch();
   const uint32_t tmem = *tmem_slot;
   int32_t pfx = 0, lo_min = 0, lo_max = 0, npt = 0, lt = 0;   // MOD: tiles [0, npt), then lt ..
-  if constexpr (MOD) {
+  auto tiles_seen = [&](int least, int most) {
     pfx = view_prefix(p, b, Lb);
-    lo_min = min(min(wlo[0], wlo[1]), min(wlo[2], wlo[3]));
-    lo_max = max(max(wlo[4], wlo[5]), max(wlo[6], wlo[7]));
+    lo_min = least;
+    lo_max = most;
     npt = (pfx + KT - 1) / KT;
     lt = lo_min < INT32_MAX ? lo_min / KT : nkt;
     lt = max(lt, npt);
     nkt = npt + max(0, nkt - lt);
-  }
+  };
+  if constexpr (MOD && !PERS)
+    tiles_seen(min(min(wlo[0], wlo[1]), min(wlo[2], wlo[3])),
+               max(max(wlo[4], wlo[5]), max(wlo[6], wlo[7])));
+  // PERS: this warp's next item, number it; false: none is left (or a wait failed).  whole: the
+  // warp takes it together, which the reductions tell the compiler (loops over the item's
+  // tiles stay in uniform registers)
+  auto take_item = [&](int it, auto whole) {
+    const bool ok = mbar_wait(&item_full[it & 1], (it >> 1) & 1, abort_flag, p.dev_err);
+    const int* m = items + (it & 1) * L::ITEM;
+    auto get = [&](int x) {
+      if constexpr (decltype(whole)::value) return __reduce_max_sync(0xffffffffu, x);
+      else return x;
+    };
+    nkt = get(ok ? m[0] : -1);
+    b = get(m[1]);
+    h = get(m[2]);
+    row0 = get(m[3]);
+    i0 = get(m[4]);
+    n = get(m[5]);
+    P0 = get(m[6]);
+    nblk = get(m[7]);
+    pfx = get(m[8]);
+    lo_max = get(m[9]);
+    lt = get(m[10]);
+    npt = (pfx + KT - 1) / KT;
+    return nkt >= 0;
+  };
   // key tile number j of this CTA.  MOD: the nearest first, so that under a bias the running
   // maximum settles with the first tile (it would grow, and the accumulator be rescaled, with
   // every tile that comes nearer)
@@ -233,16 +296,16 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
   auto sees_whole = [&](int t0, uint32_t bad) {
     return bad == 0 && (t0 + KT <= pfx || (lo_max <= t0 && t0 + KT - 1 <= P0 + i0));
   };
-  // MOD: zeroes the value rows of tile j's keys whose bit is set, by n threads (this one: tid)
-  auto zero_values = [&](int j, const uint32_t (&keys)[4], int tid, int n) {
-    uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
-    for (int idx = tid; idx < KT * NG * 8; idx += n) {
+  // MOD: zeroes the value rows of tile g's keys whose bit is set, by nt threads (this one: tid)
+  auto zero_values = [&](int g, const uint32_t (&keys)[4], int tid, int nt) {
+    uint8_t* vst = sm + L::ST_OFF + (g % NS) * L::STAGE + L::K_BYTES;
+    for (int idx = tid; idx < KT * NG * 8; idx += nt) {
       const int tok = idx / (NG * 8);
       const uint32_t w = tok < 64 ? (tok < 32 ? keys[0] : keys[1]) : (tok < 96 ? keys[2] : keys[3]);
       if (!((w >> (tok & 31)) & 1u)) continue;
       const int rem = idx % (NG * 8);
-      const int g = rem >> 3, ch = rem & 7;
-      *reinterpret_cast<uint4*>(vst + (g * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
+      const int box = rem >> 3, ch = rem & 7;
+      *reinterpret_cast<uint4*>(vst + (box * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
                                 (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
     }
   };
@@ -252,38 +315,86 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     // that page's copy (the eight small copies of a tile set the kernel's pace when one
     // thread issues them in turn); lane 0 waits for the stage and arms its byte count.
     constexpr int BPT = KT / kBlockSize;                  // pages per key tile
-    if (lane == 0) {
-      prefetch_tmap(&kp_map);
-      mbar_arrive_expect_tx(q_full, 2 * L::Q_BYTES);
-      tma_load_2d(sm, &qhi_map, h * 64, row0, q_full);
-      tma_load_2d(sm + L::Q_BYTES, &qlo_map, h * 64, row0, q_full);
-    }
-    const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-    const int pg0 = tile_of(0) * BPT + lane;
-    int32_t nxt = (lane < BPT && nkt > 0 && page_read(pg0)) ? table[pg0] : -1;
-    for (int j = 0; j < nkt; ++j) {
-      const int s = j % NS;
-      const bool mine = lane < BPT && page_read(tile_of(j) * BPT + lane);
-      int32_t phys = mine ? nxt : -1;
-      if (mine && (phys < 0 || phys >= p.num_blocks)) {
-        atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
-        phys = -1;
+    if (lane == 0) prefetch_tmap(&kp_map);
+    auto load_queries = [&](int qb, uint64_t* full) {
+      mbar_arrive_expect_tx(full, 2 * L::Q_BYTES);
+      tma_load_2d(sm + qb * 2 * L::Q_BYTES, &qhi_map, h * 64, row0, full);
+      tma_load_2d(sm + qb * 2 * L::Q_BYTES + L::Q_BYTES, &qlo_map, h * 64, row0, full);
+    };
+    if (!PERS && lane == 0) load_queries(0, q_full);
+    bool ok = true;
+    [[maybe_unused]] int nq = 0;                          // PERS: items with key tiles
+    for (int it = 0, g0 = 0; ok; ++it) {                  // g0: tiles of the items before
+      if constexpr (PERS) {
+        int w = blockIdx.x;
+        if (it > 0) {
+          if (lane == 0) w = gridDim.x + atomicAdd(p.tcount + 1, 1);
+          w = __shfl_sync(0xffffffffu, w, 0);
+        }
+        const bool more = w / H < *p.tcount;
+        if (more) {
+          h = w % H;
+          locate(w / H);
+          int32_t least = INT32_MAX, most = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = 32 * k + lane;
+            const int32_t f = i0 + r < n ? view_begin(p, row0 + r, P0 + i0 + r) : 0;
+            if (i0 + r < n && f <= P0 + i0 + r) least = min(least, f);
+            most = max(most, f);
+          }
+          tiles_seen(__reduce_min_sync(0xffffffffu, least), __reduce_max_sync(0xffffffffu, most));
+        } else {
+          nkt = -1;
+        }
+        if (it >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(&item_empty[it & 1], ((it - 2) >> 1) & 1,
+                                                 abort_flag, p.dev_err));
+        if (!ok) break;
+        if (lane == 0) {
+          int* m = items + (it & 1) * L::ITEM;
+          const int v[L::ITEM] = {nkt, b, h, row0, i0, n, P0, nblk, pfx, lo_max, lt, nq};
+#pragma unroll
+          for (int k = 0; k < L::ITEM; ++k) m[k] = v[k];
+          mbar_arrive(&item_full[it & 1]);
+        }
+        if (!more) break;
+        if (nkt == 0) continue;
+        if (nq >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[nq & 1], ((nq - 2) >> 1) & 1, abort_flag,
+                                                 p.dev_err));
+        if (!ok) break;
+        if (lane == 0) load_queries(nq & 1, nq & 1 ? q_full2 : q_full);
+        ++nq;
       }
-      const int nb = tile_of(j + 1) * BPT + lane;          // the next tile's page, in flight
-      nxt = (lane < BPT && j + 1 < nkt && page_read(nb)) ? table[nb] : -1;
-      // MOD: rejected pages, for the softmax to mask (keys run at most NS + 2 tiles ahead of it)
-      const uint32_t rejected = MOD ? __ballot_sync(0xffffffffu, mine && phys < 0) : 0;
-      const int nload = __popc(__ballot_sync(0xffffffffu, phys >= 0));
-      bool ok = true;
-      if (lane == 0) {
-        ok = j < NS || mbar_wait(&k_empty[s], ((j / NS) - 1) & 1, abort_flag, p.dev_err);
-        if constexpr (MOD) kbad[j & 7] = static_cast<int>(rejected);
-        if (ok) mbar_arrive_expect_tx(&k_full[s], nload * 2048);
+      const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
+      const int pg0 = tile_of(0) * BPT + lane;
+      int32_t nxt = (lane < BPT && nkt > 0 && page_read(pg0)) ? table[pg0] : -1;
+      for (int j = 0; ok && j < nkt; ++j) {
+        const int g = g0 + j, s = g % NS;
+        const bool mine = lane < BPT && page_read(tile_of(j) * BPT + lane);
+        int32_t phys = mine ? nxt : -1;
+        if (mine && (phys < 0 || phys >= p.num_blocks)) {
+          atomicOr(p.dev_err, RCP_DEVERR_BAD_BLOCK);
+          phys = -1;
+        }
+        const int nb = tile_of(j + 1) * BPT + lane;        // the next tile's page, in flight
+        nxt = (lane < BPT && j + 1 < nkt && page_read(nb)) ? table[nb] : -1;
+        // MOD: rejected pages, for the softmax to mask (keys run at most NS + 2 tiles ahead of it)
+        const uint32_t rejected = MOD ? __ballot_sync(0xffffffffu, mine && phys < 0) : 0;
+        const int nload = __popc(__ballot_sync(0xffffffffu, phys >= 0));
+        if (lane == 0) {
+          ok = g < NS || mbar_wait(&k_empty[s], ((g / NS) - 1) & 1, abort_flag, p.dev_err);
+          if constexpr (MOD) kbad[g & 7] = static_cast<int>(rejected);
+          if (ok) mbar_arrive_expect_tx(&k_full[s], nload * 2048);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);             // the byte count is armed first
+        if (ok && phys >= 0)
+          tma_load_2d(sm + L::ST_OFF + s * L::STAGE + lane * 2048, &kp_map, 0,
+                      (phys * H + h) * kBlockSize, &k_full[s]);
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;   // the byte count is armed first
-      if (phys >= 0)
-        tma_load_2d(sm + L::ST_OFF + s * L::STAGE + lane * 2048, &kp_map, 0,
-                    (phys * H + h) * kBlockSize, &k_full[s]);
+      g0 += nkt;
+      if constexpr (!PERS) break;
     }
   } else if (warp == 2 + NSW) {
     // ---------------------------------------------------------------- value copies
@@ -291,18 +402,33 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
       // V^ rows of the request are contiguous: one 64-column box of 128 keys per group
       if (lane == 0) {
         prefetch_tmap(&vp_map);
-        for (int j = 0; j < nkt; ++j) {
-          const int s = j % NS;
-          uint8_t* vst = sm + L::ST_OFF + s * L::STAGE + L::K_BYTES;
-          if (j >= NS && !mbar_wait(&v_empty[s], ((j / NS) - 1) & 1, abort_flag, p.dev_err)) break;
-          mbar_arrive_expect_tx(&v_full[s], NG * KT * 128);
-          // MOD: V^ holds the tiles that some row of the request sees
-          const int vt = MOD ? TileMap<S>(p.vmap + 2 * b, nblk).compact(tile_of(j)) : j;
-          const int64_t vrow = p.vcum[b] * kBlockSize + static_cast<int64_t>(vt) * KT;
+        bool ok = true;
+        for (int it = 0, g0 = 0; ok; ++it) {
+          if constexpr (PERS) {
+            if (!take_item(it, std::false_type{})) break;
+            mbar_arrive(&item_empty[it & 1]);
+          }
+          const int64_t first = p.vcum[b] * kBlockSize;
+          int tile0 = 0;                                // MOD: the tiles between npt and lt
+          if constexpr (MOD) {                          // ... are not in V^
+            const TileMap<S> map(p.vmap + 2 * b, nblk);
+            tile0 = map.lt - map.np;
+          }
+          for (int j = 0; j < nkt; ++j) {
+            const int g = g0 + j, s = g % NS;
+            uint8_t* vst = sm + L::ST_OFF + s * L::STAGE + L::K_BYTES;
+            ok = g < NS || mbar_wait(&v_empty[s], ((g / NS) - 1) & 1, abort_flag, p.dev_err);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&v_full[s], NG * KT * 128);
+            const int x = tile_of(j);
+            const int64_t vrow = first + static_cast<int64_t>(MOD && x >= npt ? x - tile0 : x) * KT;
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
-            tma_load_2d(vst + g * KT * 128, &vp_map, h * D + g * 64, static_cast<int32_t>(vrow),
-                        &v_full[s]);
+            for (int q = 0; q < NG; ++q)
+              tma_load_2d(vst + q * KT * 128, &vp_map, h * D + q * 64, static_cast<int32_t>(vrow),
+                          &v_full[s]);
+          }
+          g0 += nkt;
+          if constexpr (!PERS) break;
         }
       }
     } else {
@@ -361,7 +487,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
       constexpr uint32_t id_s = make_idesc_f16(128, KT, false, false);
       constexpr uint32_t id_pv = make_idesc_f16(128, VN, false, true);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t qd = make_sdesc(smem_u32(sm), 16, 1024, kSwizzle128B);
+      const uint64_t qd0 = make_sdesc(smem_u32(sm), 16, 1024, kSwizzle128B);
       const uint64_t pd = make_sdesc(smem_u32(sm + L::P_OFF), 16, 1024, kSwizzle128B);
       const uint64_t kd0 = make_sdesc(smem_u32(sm + L::ST_OFF), 16, 1024, kSwizzle128B);
       const uint64_t vd0 = make_sdesc(smem_u32(sm + L::ST_OFF + L::K_BYTES),
@@ -369,42 +495,87 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
       int ks = 0, vs = 0;                // stages of the next keys and values
       uint32_t kph = 0, vph = 0;         // their phases
       const bool leader = elect_one();
-      auto scores = [&](int j) {
-        const int g = j & 1;
-        const bool go = mbar_wait(&k_full[ks], kph, abort_flag, p.dev_err);
-        if (!__all_sync(0xffffffffu, go)) return false;
+      bool ok = true;
+      int gs = 0;                        // tiles whose scores have been issued
+      int js = 0, ns = PERS ? 0 : nkt;   // the next one's number in its item, the item's tiles
+      int its = 0, nq = 0;               // PERS: items read, those with key tiles before this one
+      bool last = !PERS;                 // PERS: no item is left
+      uint32_t ends = 0;                 // PERS: an item's first (1) and last (2) tile, by tile & 1
+      // the item of the next scores; false: none is left, or it is not there yet and block is
+      // false (while a tile is in flight, whose values this warp has to add first: an item
+      // that is late may be waiting for that tile's softmax)
+      auto item = [&](bool block) {
+        while (PERS && js == ns && !last) {
+          uint64_t* full = &item_full[its & 1];
+          const uint32_t ph = (its >> 1) & 1;
+          if (!__all_sync(0xffffffffu, mbar_test_wait(full, ph))) {
+            if (!block) return false;
+            ok = __all_sync(0xffffffffu, mbar_wait(full, ph, abort_flag, p.dev_err));
+            if (!ok) return false;
+          }
+          ns = __reduce_max_sync(0xffffffffu, items[(its & 1) * L::ITEM]);   // (uniform, as below)
+          if (lane == 0) mbar_arrive(&item_empty[its & 1]);
+          ++its;
+          js = 0;
+          if (ns < 0) {
+            last = true;
+            ns = 0;
+          } else if (ns > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(nq & 1 ? q_full2 : q_full, (nq >> 1) & 1,
+                                                   abort_flag, p.dev_err));
+            if (!ok) return false;
+          }
+        }
+        return js < ns;
+      };
+      auto scores = [&](bool block) {   // whether it issued a tile's scores
+        if (!item(block)) return false;
+        const int g = gs & 1, qb = PERS ? nq & 1 : 0;
+        ok = __all_sync(0xffffffffu, mbar_wait(&k_full[ks], kph, abort_flag, p.dev_err));
+        if (!ok) return false;
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (L::STAGE >> 4));
+        const uint64_t qd = qd0 + static_cast<uint64_t>(qb * (2 * L::Q_BYTES >> 4));
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             umma_f16(tm + g * 128, qd + kk * 2, kd + kk * 2, id_s, kk > 0 ? 1u : 0u);
             umma_f16(tm + g * 128, qd + (L::Q_BYTES >> 4) + kk * 2, kd + kk * 2, id_s, 1u);
           }
-          sbad[g] = kbad[j & 7];
+          sbad[g] = kbad[gs & 7];
           mbar_arrive(&s_full[g]);
           umma_commit(&s_full[g]);
           umma_commit(&k_empty[ks]);
+          if (PERS && js + 1 == ns) umma_commit(&q_empty[qb]);
         }
         __syncwarp();
+        if constexpr (PERS)
+          ends = (ends & ~(3u << (2 * g))) |
+                 ((js == 0 ? 1u : 0u) | (js + 1 == ns ? 2u : 0u)) << (2 * g);
+        ++gs;
+        if (++js == ns) ++nq;
         if (++ks == NS) {
           ks = 0;
           kph ^= 1;
         }
         return true;
       };
-      bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.dev_err));
-      ok = ok && (nkt < 1 || scores(0)) && (nkt < 2 || scores(1));
-      for (int j = 0; ok && j < nkt; ++j) {
-        // RECON: P buffer j & 1, each with its own barriers; rank space: one P buffer
-        const int pb = RECON ? (j & 1) : 0;
+      if constexpr (!PERS)
+        ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.dev_err));
+      if (ok && scores(true)) scores(false);
+      for (int g = 0; ok; ++g) {
+        // nothing in flight: the next item, or the end
+        if (g == gs && !scores(true)) break;
+        // RECON: P buffer g & 1, each with its own barriers; rank space: one P buffer
+        const int pb = RECON ? (g & 1) : 0;
         ok = mbar_wait(&v_full[vs], vph, abort_flag, p.dev_err);
-        ok = mbar_wait(&p_full[pb], RECON ? (j >> 1) & 1 : j & 1, abort_flag, p.dev_err) && ok;
+        ok = mbar_wait(&p_full[pb], RECON ? (g >> 1) & 1 : g & 1, abort_flag, p.dev_err) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (L::STAGE >> 4));
-        const uint32_t more = j > 0 ? 1u : 0u;
+        const uint32_t end = PERS ? (ends >> (2 * (g & 1))) & 3u : (g == 0 ? 1u : 0u);
+        const uint32_t more = (end & 1u) ^ 1u;
         if (leader) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k) {
@@ -417,15 +588,18 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
           }
           umma_commit(&pv_done[pb]);
           umma_commit(&v_empty[vs]);
+          if (PERS && (end & 2u)) umma_commit(acc_done);
         }
         __syncwarp();
         if (++vs == NS) {
           vs = 0;
           vph ^= 1;
         }
-        if (j + 2 < nkt) ok = scores(j + 2);
+        // the scores' buffers of tiles up to g have been read
+        while (ok && gs < g + 3 && scores(false)) {
+        }
       }
-      if (leader) umma_commit(acc_done);
+      if (!PERS && leader) umma_commit(acc_done);
     }
     if (!(MOD && RECON) && lane == 0) {
       constexpr uint32_t id_s = make_idesc_f16(128, KT, false, false);
@@ -520,260 +694,314 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     const int hf = HALVES > 1 ? (warp - 2) >> 2 : 0;    // half of the tile's keys
     constexpr int KC = KT / HALVES, VC = VN / HALVES;   // this thread's keys, value columns
     const int r = quarter * 32 + lane;                  // query row within the tile
-    const int ci = i0 + r;                              // chunk row
-    const bool row_ok = ci < n;
-    const int pos = P0 + ci;                            // keys 0 .. pos are attended
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    float m_run = -INFINITY, l_run = 0.f;
-    [[maybe_unused]] RowMod rm(p, h, MOD && row_ok, row0 + r, pos, pfx);
-    uint8_t* pbuf = sm + L::P_OFF;
-    for (int j = 0; j < nkt; ++j) {
-      const int s = j & 1;
-      bool ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], (j >> 1) & 1, abort_flag, p.dev_err));
-      tc_fence_after();
-      const int lim = row_ok ? pos - j * KT : -1;       // columns 0 .. lim are valid
-      // the whole 128-column score row: eight loads in flight, one wait
-      float sv[KC];
-      if (ok) {
-#pragma unroll
-        for (int c = 0; c < KC; c += 16)
-          tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+    for (int it = 0, g0 = 0;; ++it) {                   // g0: tiles of the items before
+      if constexpr (PERS) {
+        const bool more = take_item(it, std::true_type{});
+        if (!more) break;
       }
-      const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key,
-      const int h0 = t0 + hf * KC;                      // ... and this thread's
-      uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
-      uint32_t seen[KC / 32] = {};                      // MOD: keys that this row sees (edge)
-      bool whole = true, edge = false;
-      float shift = 0.f;                                // MOD: to be added to every score
-      if constexpr (MOD) {   // while the scores are on their way
-        const uint32_t bad = static_cast<uint32_t>(sbad[s]);
-        whole = sees_whole(t0, bad);
-        edge = !ok || !row_ok || !whole;
-        if (!whole && ok && row_ok) {
-#pragma unroll
-          for (int k = 0; k < KC / 32; ++k)
-            seen[k] = rm.seen(h0 + 32 * k, bad >> ((hf * KC + 32 * k) / kBlockSize));
-        }
-      }
-      if (ok) tmem_wait_ld();
-      if constexpr (MOD) {
-        shift = modify_scores(sv, p, rm, h0, edge, seen, [&]() {
+      const int ci = i0 + r;                              // chunk row
+      const bool row_ok = ci < n;
+      const int pos = P0 + ci;                            // keys 0 .. pos are attended
+      float m_run = -INFINITY, l_run = 0.f;
+      [[maybe_unused]] RowMod rm(p, h, MOD && row_ok, row0 + r, pos, pfx);
+      uint8_t* pbuf = sm + L::P_OFF;
+      for (int j = 0; j < nkt; ++j) {
+        const int g = g0 + j, s = g & 1;
+        bool ok = mbar_wait(&s_full[s], (g >> 1) & 1, abort_flag, p.dev_err);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const int lim = row_ok ? pos - j * KT : -1;       // columns 0 .. lim are valid
+        // the whole 128-column score row: eight loads in flight, one wait
+        float sv[KC];
+        if (ok) {
 #pragma unroll
           for (int c = 0; c < KC; c += 16)
             tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
-          tmem_wait_ld();
-        });
-        if (!whole) {   // uniform over the softmax warps
-          uint32_t* cm = colm + s * 16;
+        }
+        const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key,
+        const int h0 = t0 + hf * KC;                      // ... and this thread's
+        uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
+        uint32_t seen[KC / 32] = {};                      // MOD: keys that this row sees (edge)
+        bool whole = true, edge = false;
+        float shift = 0.f;                                // MOD: to be added to every score
+        if constexpr (MOD) {   // while the scores are on their way
+          const uint32_t bad = static_cast<uint32_t>(sbad[s]);
+          whole = sees_whole(t0, bad);
+          edge = !ok || !row_ok || !whole;
+          if (!whole && ok && row_ok) {
 #pragma unroll
-          for (int k = 0; k < KC / 32; ++k) {
-            const uint32_t w = __reduce_or_sync(0xffffffffu, seen[k]);
-            if (lane == 0) cm[quarter * 4 + hf * (KC / 32) + k] = w;
+            for (int k = 0; k < KC / 32; ++k)
+              seen[k] = rm.seen(h0 + 32 * k, bad >> ((hf * KC + 32 * k) / kBlockSize));
           }
-          named_bar_sync(1, 32 * NSW);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
         }
-      }
-      const bool full_tile = MOD || __all_sync(0xffffffffu, lim >= KT - 1);   // below the diagonal
-      // masked columns (diagonal tiles, rows past the chunk, a failed wait) become -inf, so
-      // the max and the exponentials below need no per-element test (exp2(-inf) = 0)
-      if (!MOD && (!ok || !full_tile)) {
+        if (ok) tmem_wait_ld();
+        if constexpr (MOD) {
+          shift = modify_scores(sv, p, rm, h0, edge, seen, [&]() {
 #pragma unroll
-        for (int c = 0; c < KC; ++c) sv[c] = (ok && c <= lim) ? sv[c] : -INFINITY;
-      }
-      // row max: four independent chains of three-input maxima
-      float mx;
-      {
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int c = 0; c < KC; c += 16)
+              tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
+            tmem_wait_ld();
+          });
+          if (!whole) {   // uniform over the softmax warps
+            uint32_t* cm = colm + s * 16;
 #pragma unroll
-        for (int c = 0; c < KC; c += 8) {
-          m4[0] = max3f(m4[0], sv[c], sv[c + 1]);
-          m4[1] = max3f(m4[1], sv[c + 2], sv[c + 3]);
-          m4[2] = max3f(m4[2], sv[c + 4], sv[c + 5]);
-          m4[3] = max3f(m4[3], sv[c + 6], sv[c + 7]);
+            for (int k = 0; k < KC / 32; ++k) {
+              const uint32_t w = __reduce_or_sync(0xffffffffu, seen[k]);
+              if (lane == 0) cm[quarter * 4 + hf * (KC / 32) + k] = w;
+            }
+            named_bar_sync(1, 32 * NSW);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
+          }
         }
-        mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-        if constexpr (MOD) mx += shift;
-        if constexpr (HALVES > 1) {
-          // the row's largest: this half's and the other's
-          float* hm = half_max + (L::HB > 1 ? s * 256 : 0);
-          if (L::HB == 1) named_bar_sync(2, 32 * NSW);   // the last tile's have been read
-          hm[hf * 128 + r] = mx;
-          named_bar_sync(2, 32 * NSW);
-          mx = fmaxf(mx, hm[(hf ^ 1) * 128 + r]);
-        }
-      }
-      const float m_new = (mx > m_run + kPfRescale) ? mx : m_run;
-      const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
-      uint32_t packed[KC / 2];
-      float rsum;
-      {
-        // rows with no valid key
-        const float msub = (m_new == -INFINITY) ? 0.f : (MOD ? m_new - shift : m_new);
-        const float2 msub2 = make_float2(msub, msub);
-        float2 s4[4];
+        const bool full_tile = MOD || __all_sync(0xffffffffu, lim >= KT - 1);   // below the diagonal
+        // masked columns (diagonal tiles, rows past the chunk, a failed wait) become -inf, so
+        // the max and the exponentials below need no per-element test (exp2(-inf) = 0)
+        if (!MOD && (!ok || !full_tile)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s4[q] = make_float2(0.f, 0.f);
-        // the row sum is taken in fp32 before the weights are rounded to fp16; pairs of
-        // columns go through the packed fp32x2 add / subtract
-#pragma unroll
-        for (int c = 0; c < KC; c += 2) {
-          const float2 d = sub_f32x2(make_float2(sv[c], sv[c + 1]), msub2);
-          const float2 pp = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-          s4[(c >> 1) & 3] = add_f32x2(s4[(c >> 1) & 3], pp);
-          const __half2 hp = __floats2half2_rn(pp.x, pp.y);
-          packed[c / 2] = *reinterpret_cast<const uint32_t*>(&hp);
+          for (int c = 0; c < KC; ++c) sv[c] = (ok && c <= lim) ? sv[c] : -INFINITY;
         }
-        const float2 t2 = add_f32x2(add_f32x2(s4[0], s4[1]), add_f32x2(s4[2], s4[3]));
-        rsum = t2.x + t2.y;
-      }
-      // rank space: the previous tile's value MMA must be done before P is overwritten or
-      // Z rescaled.  RECON: P buffer j & 1 must be free (value MMA of tile j-2), and only a
-      // rescale needs the previous tile's value MMA
-      const bool rescale = __any_sync(0xffffffffu, ok && alpha != 1.f && j > 0);
-      if constexpr (RECON) {
-        if (j >= 2) ok = mbar_wait(&pv_done[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.dev_err) && ok;
-        if (rescale)
-          ok = mbar_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, p.dev_err) && ok;
-      } else {
-        if (j > 0) ok = mbar_wait(&pv_done[0], (j - 1) & 1, abort_flag, p.dev_err) && ok;
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      // tcgen05.ld / st are warp-collective: the whole warp rescales when any lane needs it
-      // (lanes whose max did not move multiply by 1)
-      if (ok && rescale) {
+        // row max: four independent chains of three-input maxima
+        float mx;
+        {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < KC; c += 8) {
+            m4[0] = max3f(m4[0], sv[c], sv[c + 1]);
+            m4[1] = max3f(m4[1], sv[c + 2], sv[c + 3]);
+            m4[2] = max3f(m4[2], sv[c + 4], sv[c + 5]);
+            m4[3] = max3f(m4[3], sv[c + 6], sv[c + 7]);
+          }
+          mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+          if constexpr (MOD) mx += shift;
+          if constexpr (HALVES > 1) {
+            // the row's largest: this half's and the other's
+            float* hm = half_max + (L::HB > 1 ? s * 256 : 0);
+            if (L::HB == 1) named_bar_sync(2, 32 * NSW);   // the last tile's have been read
+            hm[hf * 128 + r] = mx;
+            named_bar_sync(2, 32 * NSW);
+            mx = fmaxf(mx, hm[(hf ^ 1) * 128 + r]);
+          }
+        }
+        const float m_new = (mx > m_run + kPfRescale) ? mx : m_run;
+        const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
+        uint32_t packed[KC / 2];
+        float rsum;
+        {
+          // rows with no valid key
+          const float msub = (m_new == -INFINITY) ? 0.f : (MOD ? m_new - shift : m_new);
+          const float2 msub2 = make_float2(msub, msub);
+          float2 s4[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) s4[q] = make_float2(0.f, 0.f);
+          // the row sum is taken in fp32 before the weights are rounded to fp16; pairs of
+          // columns go through the packed fp32x2 add / subtract
+#pragma unroll
+          for (int c = 0; c < KC; c += 2) {
+            const float2 d = sub_f32x2(make_float2(sv[c], sv[c + 1]), msub2);
+            const float2 pp = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+            s4[(c >> 1) & 3] = add_f32x2(s4[(c >> 1) & 3], pp);
+            const __half2 hp = __floats2half2_rn(pp.x, pp.y);
+            packed[c / 2] = *reinterpret_cast<const uint32_t*>(&hp);
+          }
+          const float2 t2 = add_f32x2(add_f32x2(s4[0], s4[1]), add_f32x2(s4[2], s4[3]));
+          rsum = t2.x + t2.y;
+        }
+        // rank space: the previous tile's value MMA must be done before P is overwritten or
+        // Z rescaled.  RECON: P buffer j & 1 must be free (value MMA of tile j-2), and only a
+        // rescale needs the previous tile's value MMA
+        const bool rescale = __any_sync(0xffffffffu, ok && alpha != 1.f && j > 0);
+        if constexpr (RECON) {
+          if (g >= 2)
+            ok = mbar_wait(&pv_done[g & 1], ((g - 2) >> 1) & 1, abort_flag, p.dev_err) && ok;
+          if (rescale)
+            ok = mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, p.dev_err) && ok;
+        } else {
+          if (j > 0) ok = mbar_wait(&pv_done[0], (j - 1) & 1, abort_flag, p.dev_err) && ok;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        // tcgen05.ld / st are warp-collective: the whole warp rescales when any lane needs it
+        // (lanes whose max did not move multiply by 1)
+        if (ok && rescale) {
 #pragma unroll 1
-        for (int c = hf * VC; c < (hf + 1) * VC; c += 32) {
-          float v[16], w[16];
-          tmem_ld16(tl + 256 + c, v);
-          tmem_ld16(tl + 256 + c + 16, w);
-          tmem_wait_ld();
+          for (int c = hf * VC; c < (hf + 1) * VC; c += 32) {
+            float v[16], w[16];
+            tmem_ld16(tl + 256 + c, v);
+            tmem_ld16(tl + 256 + c + 16, w);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[e] *= alpha;
-            w[e] *= alpha;
+            for (int e = 0; e < 16; ++e) {
+              v[e] *= alpha;
+              w[e] *= alpha;
+            }
+            tmem_st16(tl + 256 + c, v);
+            tmem_st16(tl + 256 + c + 16, w);
           }
-          tmem_st16(tl + 256 + c, v);
-          tmem_st16(tl + 256 + c + 16, w);
-        }
-        tmem_wait_st();
-      }
-      if constexpr (RECON) {
-        // P row r into tensor memory lane r: column c holds keys 2c and 2c+1
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < KC / 2; c += 16)
-            tmem_st16u(tl + L::P_TM + (j & 1) * (KT / 2) + hf * (KC / 2) + c, &packed[c]);
           tmem_wait_st();
         }
-      } else {
-        // P row r, K-major, 128-byte swizzle: 16-byte chunk c of the row sits at c ^ (r % 8)
+        if constexpr (RECON) {
+          // P row r into tensor memory lane r: column c holds keys 2c and 2c+1
+          if (ok) {
 #pragma unroll
-        for (int ch = 0; ch < KC / 8; ++ch) {
-          const int kb = (hf * (KC / 8) + ch) >> 3, cc = ch & 7;
-          *reinterpret_cast<uint4*>(pbuf + kb * 16384 + r * 128 + ((cc ^ (r & 7)) << 4)) =
-              make_uint4(packed[ch * 4], packed[ch * 4 + 1], packed[ch * 4 + 2], packed[ch * 4 + 3]);
-        }
-      }
-      l_run = l_run * alpha + rsum;
-      m_run = m_new;
-      if (MOD && (unseen[0] | unseen[1] | unseen[2] | unseen[3])) {
-        // keys that no row sees (among them tokens past the end and rejected pages): the same
-        ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
-        zero_values(j, unseen, threadIdx.x - 64, 32 * NSW);
-      }
-      if (!MOD && j * KT + KT > Lb) {
-        // tokens past the end of the request: zero their value rows so that whatever the
-        // slots hold (or stale bytes of skipped pages) never meet a zero weight as 0 * NaN
-        ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
-        uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
-        const int first = Lb - j * KT > 0 ? Lb - j * KT : 0;
-        const int nrow = KT - first;
-        for (int idx = threadIdx.x - 64; idx < nrow * NG * 8; idx += 128) {   // warps 2-5
-          const int tok = first + idx / (NG * 8);
-          const int rem = idx % (NG * 8);
-          const int g = rem >> 3, ch = rem & 7;
-          *reinterpret_cast<uint4*>(vst + (g * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
-                                    (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-        }
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[RECON ? (j & 1) : 0]);
-    }
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, abort_flag, p.dev_err));
-    tc_fence_after();
-    if constexpr (HALVES > 1) {   // the halves' sums (every thread is done with its last tile)
-      half_max[hf * 128 + r] = l_run;
-      named_bar_sync(2, 32 * NSW);
-      l_run += half_max[(hf ^ 1) * 128 + r];
-    }
-    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-    if constexpr (RECON) {
-      // ------------------------------------------- O / l straight to the output rows
-      if (ok) {   // warp-uniform: every lane loads, only rows of the chunk are stored
-        __half* dst = static_cast<__half*>(p.out) + (static_cast<size_t>(row0 + r) * H + h) * D;
-#pragma unroll 1
-        for (int c = hf * (D / HALVES); c < (hf + 1) * (D / HALVES); c += 16) {
-          float v[16];
-          tmem_ld16(tl + 256 + c, v);
-          tmem_wait_ld();
-          uint32_t w8[8];
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            if (MOD && !(l_run > 0.f)) v[e] = v[e + 1] = 0.f;   // saw no key: no accumulator
-            const __half2 hv = __floats2half2_rn(v[e] * inv, v[e + 1] * inv);
-            w8[e / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+            for (int c = 0; c < KC / 2; c += 16)
+              tmem_st16u(tl + L::P_TM + (g & 1) * (KT / 2) + hf * (KC / 2) + c, &packed[c]);
+            tmem_wait_st();
           }
-          if (row_ok) {
-            *reinterpret_cast<uint4*>(dst + c) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
-          }
-        }
-      }
-    } else {
-      // ------------------------------------------- normalise z, split into fp16 hi + lo
-      uint8_t* zh = sm + L::ZH_OFF;
-      uint8_t* zl = sm + L::ZL_OFF;
-#pragma unroll 1
-      for (int c = hf * (RQ / HALVES); c < (hf + 1) * (RQ / HALVES); c += 32) {
-        float v[32];
-        if (ok) {
-          tmem_ld16(tl + 256 + c, *reinterpret_cast<float(*)[16]>(&v[0]));
-          tmem_ld16(tl + 256 + c + 16, *reinterpret_cast<float(*)[16]>(&v[16]));
-          tmem_wait_ld();
         } else {
+          // P row r, K-major, 128-byte swizzle: 16-byte chunk c of the row sits at c ^ (r % 8)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+          for (int ch = 0; ch < KC / 8; ++ch) {
+            const int kb = (hf * (KC / 8) + ch) >> 3, cc = ch & 7;
+            *reinterpret_cast<uint4*>(pbuf + kb * 16384 + r * 128 + ((cc ^ (r & 7)) << 4)) =
+                make_uint4(packed[ch * 4], packed[ch * 4 + 1], packed[ch * 4 + 2],
+                           packed[ch * 4 + 3]);
+          }
         }
-        uint32_t hw[16], lw[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          if (MOD && !(l_run > 0.f)) v[e] = v[e + 1] = 0.f;   // saw no key: no accumulator
-          const float z0 = v[e] * inv, z1 = v[e + 1] * inv;
-          const __half2 hi = __floats2half2_rn(z0, z1);
-          const float2 hb = __half22float2(hi);
-          const __half2 lo = __floats2half2_rn(z0 - hb.x, z1 - hb.y);
-          hw[e / 2] = *reinterpret_cast<const uint32_t*>(&hi);
-          lw[e / 2] = *reinterpret_cast<const uint32_t*>(&lo);
+        l_run = l_run * alpha + rsum;
+        m_run = m_new;
+        if (MOD && (unseen[0] | unseen[1] | unseen[2] | unseen[3])) {
+          // keys that no row sees (among them tokens past the end and rejected pages): the same
+          ok = mbar_wait(&v_full[g % NS], (g / NS) & 1, abort_flag, p.dev_err) && ok;
+          zero_values(g, unseen, threadIdx.x - 64, 32 * NSW);
         }
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const int ch = (c + q4 * 8) / 8;                   // 16-byte chunk index in the row
-          const int kb = ch >> 3, cc = ch & 7;
-          const int off = kb * 16384 + r * 128 + ((cc ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(zh + off) =
-              make_uint4(hw[q4 * 4], hw[q4 * 4 + 1], hw[q4 * 4 + 2], hw[q4 * 4 + 3]);
-          *reinterpret_cast<uint4*>(zl + off) =
-              make_uint4(lw[q4 * 4], lw[q4 * 4 + 1], lw[q4 * 4 + 2], lw[q4 * 4 + 3]);
+        if (!MOD && j * KT + KT > Lb) {
+          // tokens past the end of the request: zero their value rows so that whatever the
+          // slots hold (or stale bytes of skipped pages) never meet a zero weight as 0 * NaN
+          ok = mbar_wait(&v_full[j % NS], (j / NS) & 1, abort_flag, p.dev_err) && ok;
+          uint8_t* vst = sm + L::ST_OFF + (j % NS) * L::STAGE + L::K_BYTES;
+          const int first = Lb - j * KT > 0 ? Lb - j * KT : 0;
+          const int nrow = KT - first;
+          for (int idx = threadIdx.x - 64; idx < nrow * NG * 8; idx += 128) {   // warps 2-5
+            const int tok = first + idx / (NG * 8);
+            const int rem = idx % (NG * 8);
+            const int g = rem >> 3, ch = rem & 7;
+            *reinterpret_cast<uint4*>(vst + (g * (KT / kBlockSize) + tok / kBlockSize) * 2048 +
+                                      (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[RECON ? (g & 1) : 0]);
+      }
+      bool ok = true;
+      int na = 0;                                       // PERS: items with key tiles before it
+      if constexpr (PERS) {   // read again instead of holding registers through the tiles
+        const int* m = items + (it & 1) * L::ITEM;
+        h = m[2];
+        row0 = m[3];
+        i0 = m[4];
+        n = m[5];
+        na = m[11];
+      }
+      if (!PERS || nkt > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_done, na & 1, abort_flag, p.dev_err));
+        tc_fence_after();
+        if constexpr (HALVES > 1) {   // the halves' sums (every thread is done with its last tile)
+          float* hs = PERS ? half_sum : half_max;
+          hs[hf * 128 + r] = l_run;
+          named_bar_sync(2, 32 * NSW);
+          l_run += hs[(hf ^ 1) * 128 + r];
         }
       }
-      fence_proxy_async_smem();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      if constexpr (RECON) {
+        // ------------------------------------------- O / l straight to the output rows
+        if (ok) {   // warp-uniform: every lane loads, only rows of the chunk are stored
+          __half* dst = static_cast<__half*>(p.out) + (static_cast<size_t>(row0 + r) * H + h) * D;
+          // PERS: through this item's query buffer, from which a warp stores whole 128-byte
+          // pieces of rows (16-byte chunk c of a row's half at c ^ (r % HC)); a lane storing its
+          // own row takes a memory access per row and chunk, 3500 cycles of the tile against 1900
+          constexpr int HC = D / 8 / HALVES;               // 16-byte chunks of a half
+          uint8_t* stage = sm + (na & 1) * 2 * L::Q_BYTES + quarter * 32 * D * 2 + hf * HC * 16;
+#pragma unroll 1
+          for (int c = hf * (D / HALVES); c < (hf + 1) * (D / HALVES); c += 16) {
+            float v[16];
+            tmem_ld16(tl + 256 + c, v);
+            tmem_wait_ld();
+            uint32_t w8[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              if (MOD && !(l_run > 0.f)) v[e] = v[e + 1] = 0.f;   // saw no key: no accumulator
+              const __half2 hv = __floats2half2_rn(v[e] * inv, v[e + 1] * inv);
+              w8[e / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            const uint4 w0 = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+            const uint4 w1 = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+            if (PERS && nkt > 0) {
+              const int k = c / 8 - hf * HC, x = lane & (HC - 1);
+              *reinterpret_cast<uint4*>(stage + lane * D * 2 + ((k ^ x) << 4)) = w0;
+              *reinterpret_cast<uint4*>(stage + lane * D * 2 + (((k + 1) ^ x) << 4)) = w1;
+            } else if (i0 + r < n) {
+              *reinterpret_cast<uint4*>(dst + c) = w0;
+              *reinterpret_cast<uint4*>(dst + c + 8) = w1;
+            }
+          }
+          if (PERS && nkt > 0) {
+            __syncwarp();
+            const int k = lane % HC;
+            dst = static_cast<__half*>(p.out) + (static_cast<size_t>(row0) * H + h) * D +
+                  (hf * HC + k) * 8;
+#pragma unroll
+            for (int x0 = 0; x0 < 32; x0 += 32 / HC) {
+              const int x = x0 + lane / HC, row = quarter * 32 + x;
+              const uint4 w =
+                  *reinterpret_cast<const uint4*>(stage + x * D * 2 + ((k ^ (x & (HC - 1))) << 4));
+              if (i0 + row < n)
+                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * H * D) = w;
+            }
+            fence_proxy_async_smem();   // the next queries arrive by the async proxy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_empty[na & 1]);
+          }
+        }
+      } else {
+        // ------------------------------------------- normalise z, split into fp16 hi + lo
+        uint8_t* zh = sm + L::ZH_OFF;
+        uint8_t* zl = sm + L::ZL_OFF;
+#pragma unroll 1
+        for (int c = hf * (RQ / HALVES); c < (hf + 1) * (RQ / HALVES); c += 32) {
+          float v[32];
+          if (ok) {
+            tmem_ld16(tl + 256 + c, *reinterpret_cast<float(*)[16]>(&v[0]));
+            tmem_ld16(tl + 256 + c + 16, *reinterpret_cast<float(*)[16]>(&v[16]));
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+          }
+          uint32_t hw[16], lw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            if (MOD && !(l_run > 0.f)) v[e] = v[e + 1] = 0.f;   // saw no key: no accumulator
+            const float z0 = v[e] * inv, z1 = v[e + 1] * inv;
+            const __half2 hi = __floats2half2_rn(z0, z1);
+            const float2 hb = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(z0 - hb.x, z1 - hb.y);
+            hw[e / 2] = *reinterpret_cast<const uint32_t*>(&hi);
+            lw[e / 2] = *reinterpret_cast<const uint32_t*>(&lo);
+          }
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int ch = (c + q4 * 8) / 8;                   // 16-byte chunk index in the row
+            const int kb = ch >> 3, cc = ch & 7;
+            const int off = kb * 16384 + r * 128 + ((cc ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(zh + off) =
+                make_uint4(hw[q4 * 4], hw[q4 * 4 + 1], hw[q4 * 4 + 2], hw[q4 * 4 + 3]);
+            *reinterpret_cast<uint4*>(zl + off) =
+                make_uint4(lw[q4 * 4], lw[q4 * 4 + 1], lw[q4 * 4 + 2], lw[q4 * 4 + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(zq_full);
+      }
+      if constexpr (!PERS) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(zq_full);
+      if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+      g0 += nkt;
     }
   }
   __syncwarp();
@@ -863,10 +1091,13 @@ cudaError_t prepare_prefill() {
   auto set = [](auto kernel, int smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
-  cudaError_t e = set(prefill_kernel<S, false, false>, PfSmem<S, false>::ALLOC);
-  if (e == cudaSuccess) e = set(prefill_kernel<S, true, false>, PfSmem<S, true>::ALLOC);
-  if (e == cudaSuccess) e = set(prefill_kernel<S, false, true>, PfSmem<S, false, true>::ALLOC);
-  if (e == cudaSuccess) e = set(prefill_kernel<S, true, true>, PfSmem<S, true, true>::ALLOC);
+  cudaError_t e = set(prefill_kernel<S, false, false, false>, PfSmem<S, false>::ALLOC);
+  if (e == cudaSuccess) e = set(prefill_kernel<S, true, false, false>, PfSmem<S, true>::ALLOC);
+  if (e == cudaSuccess)
+    e = set(prefill_kernel<S, false, true, false>, PfSmem<S, false, true>::ALLOC);
+  if (e == cudaSuccess) e = set(prefill_kernel<S, true, true, false>, PfSmem<S, true, true>::ALLOC);
+  if (e == cudaSuccess)
+    e = set(prefill_kernel<S, true, true, true>, PfSmem<S, true, true, true>::ALLOC);
   return e;
 }
 
@@ -874,13 +1105,9 @@ cudaError_t prepare_prefill() {
 template <class S>
 cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const CUtensorMap& kp,
                            const CUtensorMap& vp, const CUtensorMap& w, const AttnParams& p,
-                           int max_tiles, cudaStream_t stream, bool pdl, bool recon) {
+                           int max_tiles, int num_sms, cudaStream_t stream, bool pdl, bool recon) {
   const int NQ = recon ? 1 : PrefillCfg<S>::NQ;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(max_tiles * S::H * NQ);
-  cfg.blockDim = dim3(p.mod ? PfWarps<true>::THREADS : PfWarps<false>::THREADS);
-  cfg.dynamicSmemBytes = p.mod ? (recon ? PfSmem<S, true, true>::ALLOC : PfSmem<S, false, true>::ALLOC)
-                               : (recon ? PfSmem<S, true>::ALLOC : PfSmem<S, false>::ALLOC);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   int na = 0;
@@ -896,22 +1123,39 @@ cudaError_t launch_prefill(const CUtensorMap& qhi, const CUtensorMap& qlo, const
   }
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  if (p.mod)
-    return recon ? cudaLaunchKernelEx(&cfg, prefill_kernel<S, true, true>, qhi, qlo, kp, vp, w, p)
-                 : cudaLaunchKernelEx(&cfg, prefill_kernel<S, false, true>, qhi, qlo, kp, vp, w, p);
-  if (recon) return cudaLaunchKernelEx(&cfg, prefill_kernel<S, true, false>, qhi, qlo, kp, vp, w, p);
-  return cudaLaunchKernelEx(&cfg, prefill_kernel<S, false, false>, qhi, qlo, kp, vp, w, p);
+  auto go = [&](auto kernel, int ctas, int threads, int smem) {
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, kernel, qhi, qlo, kp, vp, w, p);
+  };
+  constexpr int T = PfWarps<false>::THREADS, TM = PfWarps<true>::THREADS;
+  const int ctas = max_tiles * S::H * NQ;
+  if (!p.mod)
+    return recon ? go(prefill_kernel<S, true, false, false>, ctas, T, PfSmem<S, true>::ALLOC)
+                 : go(prefill_kernel<S, false, false, false>, ctas, T, PfSmem<S, false>::ALLOC);
+  if (!recon)
+    return go(prefill_kernel<S, false, true, false>, ctas, TM, PfSmem<S, false, true>::ALLOC);
+  // (query tile, head) items: of n rows a request has at most (n + 127) / 128 tiles.  Where every
+  // item has an SM of its own, a CTA per item starts sooner (500 rows of one request behind
+  // 32500 tokens 140 us against 142, 5-row chunks of four requests 53.5 against 55); with more
+  // items than SMs the CTAs take them in turn (2 x 4096 above; 16 x (4096 + 256) within 1 %).
+  const int64_t items = (p.nq + int64_t{127} * p.batch) / 128 * S::H;
+  if (items <= num_sms)
+    return go(prefill_kernel<S, true, true, false>, static_cast<int>(items), TM,
+              PfSmem<S, true, true>::ALLOC);
+  return go(prefill_kernel<S, true, true, true>, num_sms, TM, PfSmem<S, true, true, true>::ALLOC);
 }
 
 template cudaError_t prepare_prefill<ShapeMain>();
 template cudaError_t prepare_prefill<ShapeTiny>();
 template cudaError_t launch_prefill<ShapeMain>(const CUtensorMap&, const CUtensorMap&,
                                                const CUtensorMap&, const CUtensorMap&,
-                                               const CUtensorMap&, const AttnParams&, int,
+                                               const CUtensorMap&, const AttnParams&, int, int,
                                                cudaStream_t, bool, bool);
 template cudaError_t launch_prefill<ShapeTiny>(const CUtensorMap&, const CUtensorMap&,
                                                const CUtensorMap&, const CUtensorMap&,
-                                               const CUtensorMap&, const AttnParams&, int,
+                                               const CUtensorMap&, const AttnParams&, int, int,
                                                cudaStream_t, bool, bool);
 
 }  // namespace rcp

@@ -37,7 +37,7 @@ __device__ __forceinline__ int32_t bias_origin(RowView v, int32_t pos) {
 // A prefill request's key tiles (KT keys) that some of its rows sees: those of the prefix and
 // those from the least first token of any row on, from the plan's (prefix, least first token).
 // Their pages, one after another, are the rows of V^ (reconstructing variant) and the pages
-// the widening pass copies; key tile x is number compact(x) among them.
+// the widening pass copies; key tile x is number x among them, or x - (lt - np) past the prefix.
 template <class S>
 struct TileMap {
   static constexpr int KT = PrefillCfg<S>::KT, BPT = KT / kBlockSize;
@@ -52,9 +52,6 @@ struct TileMap {
   __device__ __forceinline__ int32_t pages() const {
     const int32_t a = np * BPT < nblk ? np * BPT : nblk, b = nblk - lt * BPT;
     return a + (b > 0 ? b : 0);
-  }
-  __device__ __forceinline__ int32_t compact(int32_t tile) const {
-    return tile < np ? tile : np + (tile - lt);
   }
   // page of the request that is number j of them
   __device__ __forceinline__ int32_t page(int32_t j) const {

@@ -114,7 +114,7 @@ inline WsLayout ws_layout(int64_t nq) {
   w.qt = o;   o = align256(o + qt_row * nq);
   w.tile_b = o;  o = align256(o + sizeof(int32_t) * prefill_max_tiles(nq));
   w.tile_qt = o; o = align256(o + sizeof(int32_t) * prefill_max_tiles(nq));
-  w.tcount = o;  o = align256(o + sizeof(int32_t));
+  w.tcount = o;  o = align256(o + 2 * sizeof(int32_t));
   // decode only from here on: split-K partial records, one per (request, partition)
   // segment, at index request + partition
   w.rec = o;  o = align256(o + sizeof(float) * (nq + kMaxParts) * static_cast<size_t>(S::REC));
@@ -179,7 +179,7 @@ struct AttnParams {
   // prefill only (nullptr for decode)
   int32_t* tile_b;            // [max tiles] request of each 128-row query tile
   int32_t* tile_qt;           // [max tiles] tile index within its request
-  int32_t* tcount;            // [1] number of query tiles
+  int32_t* tcount;            // [2] number of query tiles; items taken past a CTA's first (MOD)
   void* qhi;                  // [nq][H][64] fp16 rank-space queries (scaled), zero past r_k
   void* qlo;                  // [nq][H][64] fp16 remainder q~ - qhi
   // reconstructing prefill only (nullptr otherwise)
