@@ -27,7 +27,7 @@
 //                   a token that the row sees, the scores are capped and biased before the
 //                   softmax, and a page's tokens are attended by a bit mask.  Capped, 64 x
 //                   8192: fp16 501 us (HBM, 0.95 of the copy rate), E4M3 335 us (328 plain),
-//                   4-bit 585 us (555).  A window of 1000 tokens, E4M3: 59 us of this
+//                   4-bit 574 us (555).  A window of 1000 tokens, E4M3: 59 us of this
 //                   kernel in a step of 86.
 //   C. (combine.cu) the split-K combine, merging each request's records in a fixed order
 //                   (deterministic), fused with o_h = W_v[:, h*d:(h+1)*d]^T z_h on tensor
@@ -771,7 +771,10 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
   int* dec_n = oinfo + KST; // SKIP: valid tokens of each kept page of the decision ring
   int* sphys = dec_n + L::DS;   // SKIP + TSC: physical block of the page in each score buffer
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // MOD, quantized pages: by a shuffle, which tells the compiler that a warp's role is uniform
+  // (64 x 8192, capped: 4-bit 585 -> 574 us; fp16 loses 1 % by it)
+  const int warp = MOD && F8 ? __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0) : threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
   // prologue: nothing here reads what the previous kernel writes
