@@ -27,7 +27,7 @@
 //                   a token that the row sees, the scores are capped and biased before the
 //                   softmax, and a page's tokens are attended by a bit mask.  Capped, 64 x
 //                   8192: fp16 501 us (HBM, 0.95 of the copy rate), E4M3 335 us (328 plain),
-//                   4-bit 574 us (555).  A window of 1000 tokens, E4M3: 59 us of this
+//                   4-bit 548 us (524).  A window of 1000 tokens, E4M3: 59 us of this
 //                   kernel in a step of 86.
 //   C. (combine.cu) the split-K combine, merging each request's records in a fixed order
 //                   (deterministic), fused with o_h = W_v[:, h*d:(h+1)*d]^T z_h on tensor
@@ -439,7 +439,7 @@ __device__ __forceinline__ void widen_v_int4_pairs(const uint8_t* src, uint8_t* 
                                                    int b0, int b1, int tid) {
   const int n = (b1 - b0) * kBlockSize * 4;
   const __half* scales = reinterpret_cast<const __half*>(src + Int4Page<S>::VCODES);
-#pragma unroll 8   // measured: 2 -> 652 us, 4 -> 885 us, 8 -> 588 us at batch 64 x 8192
+#pragma unroll 1
   for (int idx = tid; idx < n; idx += NT) {
     const int c16 = idx & 3, gl = (idx >> 2) & 1, tl = (idx >> 3) & 3, th = (idx >> 5) & 3;
     const int tt = th * 4 + tl, gb = b0 + (idx >> 7) * 2 + gl;
@@ -448,14 +448,14 @@ __device__ __forceinline__ void widen_v_int4_pairs(const uint8_t* src, uint8_t* 
       const uint2 raw =
           *reinterpret_cast<const uint2*>(src + tt * (S::R / 2) + gb * 32 + c16 * 8);
       const __half2 sc = __half2half2(scales[tt * (S::R / 64) + gb]);
-      lo.x = int4x2_to_half2_bits(raw.x & 0xFFu, sc);
-      lo.y = int4x2_to_half2_bits((raw.x >> 8) & 0xFFu, sc);
-      lo.z = int4x2_to_half2_bits((raw.x >> 16) & 0xFFu, sc);
-      lo.w = int4x2_to_half2_bits(raw.x >> 24, sc);
-      hi.x = int4x2_to_half2_bits(raw.y & 0xFFu, sc);
-      hi.y = int4x2_to_half2_bits((raw.y >> 8) & 0xFFu, sc);
-      hi.z = int4x2_to_half2_bits((raw.y >> 16) & 0xFFu, sc);
-      hi.w = int4x2_to_half2_bits(raw.y >> 24, sc);
+      lo.x = int4x2_to_half2_bits<0>(raw.x, sc);
+      lo.y = int4x2_to_half2_bits<1>(raw.x, sc);
+      lo.z = int4x2_to_half2_bits<2>(raw.x, sc);
+      lo.w = int4x2_to_half2_bits<3>(raw.x, sc);
+      hi.x = int4x2_to_half2_bits<0>(raw.y, sc);
+      hi.y = int4x2_to_half2_bits<1>(raw.y, sc);
+      hi.z = int4x2_to_half2_bits<2>(raw.y, sc);
+      hi.w = int4x2_to_half2_bits<3>(raw.y, sc);
     }
     uint8_t* row = vb + gb * 2048 + tt * 128;
     *reinterpret_cast<uint4*>(row + (((2 * c16) ^ (tt & 7)) << 4)) = lo;
@@ -492,10 +492,10 @@ __device__ __forceinline__ void widen_v_boxes(const uint8_t* src, uint8_t* vb, i
         const uint32_t raw = *reinterpret_cast<const uint32_t*>(src + tt * (S::R / 2) + gb * 32 + c * 4);
         const __half2 sc = __half2half2(reinterpret_cast<const __half*>(
             src + Int4Page<S>::VCODES)[tt * (S::R / 64) + gb]);
-        o.x = int4x2_to_half2_bits(raw & 0xFFu, sc);
-        o.y = int4x2_to_half2_bits((raw >> 8) & 0xFFu, sc);
-        o.z = int4x2_to_half2_bits((raw >> 16) & 0xFFu, sc);
-        o.w = int4x2_to_half2_bits(raw >> 24, sc);
+        o.x = int4x2_to_half2_bits<0>(raw, sc);
+        o.y = int4x2_to_half2_bits<1>(raw, sc);
+        o.z = int4x2_to_half2_bits<2>(raw, sc);
+        o.w = int4x2_to_half2_bits<3>(raw, sc);
       } else {
         const uint2 raw = *reinterpret_cast<const uint2*>(src + tt * S::R + gb * 64 + c * 8);
         o.x = e4m3x2_to_half2_bits(static_cast<uint16_t>(raw.x & 0xFFFFu));
@@ -535,7 +535,7 @@ __device__ __forceinline__ void widen_k_int4(const uint8_t* raw, uint8_t* op, fl
                                              int tid) {
   static_assert(S::RK == 64, "rows of 32 code bytes");
   constexpr int UNITS = S::H * kBlockSize * 2;
-#pragma unroll 8
+#pragma unroll 1   // unrolled by two, both of these loops: 15 % of a decode at 64 x 8192
   for (int u = tid; u < UNITS; u += NT) {
     const int r = u >> 1, half = u & 1;
     const uint4 w = *reinterpret_cast<const uint4*>(raw + r * 32 + half * 16);
@@ -749,7 +749,8 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
   // others the kept pages)
   constexpr int NVW = (TSC && SKIP) ? NWW - 2 : NWW;
   // (4-bit pages: the widening warps also widen the key codes, so the compute warps take
-  // 10 of the 16 value boxes: measured 521 us at batch 64 x 8192 against 588 us for none)
+  // 10 of the 16 value boxes: measured 524 us for a call at batch 64 x 8192; 12 of them 543,
+  // 8 of them 541)
   // (SKIP: all of them, in the order of the kept pages)
   constexpr int WB =
       (SKIP || (TSC && FMT == RCP_PAGES_FP8_E4M3)) ? S::NBOX : S::NBOX >= 16 ? 6 : S::NBOX;
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
   int* sphys = dec_n + L::DS;   // SKIP + TSC: physical block of the page in each score buffer
 
   // MOD, quantized pages: by a shuffle, which tells the compiler that a warp's role is uniform
-  // (64 x 8192, capped: 4-bit 585 -> 574 us; fp16 loses 1 % by it)
+  // (64 x 8192, capped, 4-bit: 585 -> 574 us when it came in; fp16 loses 1 % by it)
   const int warp = MOD && F8 ? __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0) : threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cta = blockIdx.x;

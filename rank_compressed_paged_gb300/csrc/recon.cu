@@ -421,10 +421,10 @@ __global__ void __launch_bounds__(kWidenThreads)
                                               : vsc[(e0 / S::R) * (S::R / 64) + (e0 % S::R) / 64]);
           uint4* dst = reinterpret_cast<uint4*>((key ? reinterpret_cast<__half*>(kd)
                                                      : reinterpret_cast<__half*>(vd)) + e0);
-          *dst = make_uint4(int4x2_to_half2_bits(raw & 0xFFu, sc),
-                            int4x2_to_half2_bits((raw >> 8) & 0xFFu, sc),
-                            int4x2_to_half2_bits((raw >> 16) & 0xFFu, sc),
-                            int4x2_to_half2_bits(raw >> 24, sc));
+          *dst = make_uint4(int4x2_to_half2_bits<0>(raw, sc),
+                            int4x2_to_half2_bits<1>(raw, sc),
+                            int4x2_to_half2_bits<2>(raw, sc),
+                            int4x2_to_half2_bits<3>(raw, sc));
         }
       } else {
         for (int c = threadIdx.x; c < KC + VC; c += kWidenThreads) {
