@@ -457,6 +457,61 @@ def test_prefill_step_appends_first_and_replays_on_a_side_stream(variant):
     assert torch.equal(eager, out)
 
 
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("shape_name,pages,B", [("tiny", "fp16", 90), ("tiny", "int4", 90),
+                                                ("main", "fp16", 14), ("main", "fp8_e4m3", 14)])
+def test_prefill_of_many_query_tiles_some_without_keys(shape_name, pages, B, variant):
+    """More (query tile, head) items than SMs; runs of requests whose rows see nothing, and
+    tiles of a request that see something behind tiles that do not."""
+    import torch
+    shape = SHAPES[shape_name]
+    rng = np.random.default_rng(341)
+    prior = rng.integers(0, 300, B).tolist()
+    chunk = np.where(rng.random(B) < 0.2, rng.integers(129, 400, B), rng.integers(0, 60, B)).tolist()
+    inp = wl.make_prefill_inputs(shape, prior, chunk, seed=342)
+    c = inp.cache
+    kp = wl.fp16(rng.standard_normal(c.k_pages.shape))
+    vp = wl.fp16(rng.standard_normal(c.v_pages.shape))
+    inp.kp, inp.vp = encode(pages, kp, vp)
+    begin = [np.full(n, 2 ** 31 - 1) if (b // 4) % 3 else (np.arange(n) + p) // 90 * 90
+             for b, (p, n) in enumerate(zip(prior, chunk))]
+    for b in range(0, B, 12):
+        begin[b][:128] = 2 ** 31 - 1
+    mod = dict(softcap=8.0, row_begin=np.concatenate(begin))
+    kk, vv = values(pages, shape, inp.kp, inp.vp, True)
+    ref = (*orc.prefill_attn_mod(inp.q, inp.cu_chunk_lens, kk, vv, inp.U_k, inp.W_v, c.block_table,
+                                 inp.seq_lens_after, magnitudes=True, **mod),
+           int(max(inp.seq_lens_after)))
+    cache = cache_of(pages, shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    args = (t(inp.q), t(inp.cu_chunk_lens), t(c.block_table), t(inp.seq_lens_after))
+    dev = score_mod(mod)
+    out = torch.full(inp.q.shape, float("nan"), dtype=torch.float16, device="cuda")
+    first = None
+    for _ in range(3):                  # which CTA takes an item does not show in the result
+        cache.prefill_attn(*args, out=out, variant=variant, mod=dev)
+        torch.cuda.synchronize()
+        assert cache.read_device_error() == 0
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)
+    assert_within(out.cpu().numpy(), ref, f"{shape_name} {pages} {variant}")
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+def test_prefill_bad_chunk_offsets_write_nothing(variant):
+    import torch
+    from rank_compressed_paged_gb300 import _lib
+    inp = prefill_inputs("main", "fp16")
+    cache = cache_of("fp16", inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    cu = np.asarray(inp.cu_chunk_lens).copy()
+    cu[3] = cu[2] - 1
+    out = torch.full(inp.q.shape, 7.0, dtype=torch.float16, device="cuda")
+    cache.prefill_attn(t(inp.q), t(cu), t(inp.cache.block_table), t(inp.seq_lens_after), out=out,
+                       variant=variant, mod=score_mod(dict(window=50)))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() & _lib.RCP_DEVERR_BAD_LEN
+    assert bool((out == 7.0).all())
+
+
 # ------------------------------------------------------------- biases, padding, streams, graphs
 def odd_slopes(shape):
     """Biases that grow with the distance, steep ones and none.  A prefill tile's terms reach
