@@ -28,6 +28,12 @@
 // MMA), 1 issues the MMAs (and owns TMEM), 2-5 run the softmax and the epilogue (warp w
 // serves TMEM lanes 32*(w%4) .. +31).
 //
+// Roundings: the scores, the running maximum and sum and the accumulators are fp32; the weights
+// enter the value MMA in fp16 (kind::f16 takes both operands in 16 bits), V^ is stored in fp16
+// by the reconstruction.  Each moves the output by 2.0e-4 of its norm, its own rounding to fp16
+// by 2.1e-4, together 3.5e-4; a second fp16 term of either would double the value product or
+// the V^ traffic.
+//
 // MOD (score modifications, scoremod.cuh): eight softmax warps, 2-9, two threads per row with 64
 // keys of a tile each, because one warp per scheduler cannot hide the arithmetic added to every
 // score (16 x (4096 + 256), cap + bias: 1071 -> 914 us); the value copies are warp 10's.  The

@@ -323,3 +323,25 @@ def test_fork_step_copy_on_write_compact_and_attend(pages):
         kk, vv = values(pages, shape, cache.k_pages.cpu().numpy(), cache.v_pages.cpu().numpy(), True)
         ref = orc.prefill_attn_mod(q, cu, kk, vv, U, W, table(), new, magnitudes=True, **mod)
         assert_within(out.cpu().numpy(), (*ref, max(new)), variant)
+
+
+def test_calls_on_nothing():
+    import torch
+    k, v = random_pages(SHAPES["tiny"], "fp16", 6, 1)
+    cache = new_cache(SHAPES["tiny"], "fp16", k, v)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    cache.copy_blocks(none.view(0, 2))
+    keep = torch.empty((0, 64), dtype=torch.uint8, device="cuda")
+    assert cache.compact_tokens(none.view(0, 4), none, keep).shape == (0,)
+    ids = cache.alloc_blocks(2)
+    assert cache.fork_sequence(ids, 0, children=3) == [[], [], []]
+    assert cache.fork_sequence(ids, 20, children=0) == []
+    assert cache.block_refs(ids) == [1, 1] and cache.num_free_blocks() == 4
+    for bad in (dict(ids=ids, length=33), dict(ids=ids, length=-1), dict(ids=ids, length=2 ** 32),
+                dict(ids=ids, length=20, children=-1), dict(ids=[2 ** 32], length=3)):
+        with pytest.raises(ValueError):
+            cache.fork_sequence(**bad)
+    assert cache.block_refs(ids) == [1, 1] and cache.num_free_blocks() == 4
+    torch.cuda.synchronize()
+    assert np.array_equal(raw(cache.k_pages), raw(k)) and np.array_equal(raw(cache.v_pages), raw(v))
+    assert cache.read_device_error() == 0

@@ -672,3 +672,25 @@ def test_captured_calls_keep_their_workspaces(shape_name, pages):
             assert torch.equal(out, w)
     assert cache.read_device_error() == 0
     assert all(bool((x == 255).all()) for x in junk)     # nothing wrote to memory handed on
+
+
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("tiny", "int4")])
+def test_calls_without_requests_or_rows(shape_name, pages):
+    import torch
+    shape, cache = stream_cache(shape_name, pages)
+    H, d = shape["num_heads"], shape["head_dim"]
+    q = torch.empty((0, H, d), dtype=torch.float16, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    mod = score_mod(dict(window=3, softcap=2.0, prefix_lens=[], row_begin=[]))
+    assert cache.decode_attn(q, table, none, mod=mod).shape == q.shape
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for variant in ("rank", "reconstruct", "auto"):
+        assert cache.prefill_attn(q, cu, table, none, variant=variant, mod=mod).shape == q.shape
+    # a request without chunk rows among none at all
+    cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+    lens = torch.full((1,), 20, dtype=torch.int32, device="cuda")
+    mod = score_mod(dict(window=3, softcap=2.0, prefix_lens=[7], row_begin=[]))
+    assert cache.prefill_attn(q, cu, table, lens, mod=mod).shape == q.shape
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
