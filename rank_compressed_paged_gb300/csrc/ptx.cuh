@@ -360,12 +360,15 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 // Full cluster barrier (release / acquire): every thread of every CTA must take part.
+// (The aligned forms, which the lanes of a warp have to reach together: joined first.)
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
 // The same meeting point without ordering any memory access.
 __device__ __forceinline__ void cluster_sync_relaxed() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // Shared-memory address of the same variable in the CTA of cluster rank `rank`.
@@ -438,7 +441,10 @@ __device__ __forceinline__ float2 sub_f32x2(float2 a, float2 b) {
   return *reinterpret_cast<const float2*>(&d);
 }
 
+// (bar.sync is the aligned form, which the lanes of a warp have to reach together: joined first,
+// because lanes part before it where one of them stores or each polls an mbarrier.)
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
