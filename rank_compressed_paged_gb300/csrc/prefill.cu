@@ -260,14 +260,16 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
   if constexpr (MOD && !PERS)
     tiles_seen(min(min(wlo[0], wlo[1]), min(wlo[2], wlo[3])),
                max(max(wlo[4], wlo[5]), max(wlo[6], wlo[7])));
-  // PERS: this warp's next item, number it; false: none is left (or a wait failed).  whole: the
-  // warp takes it together, which the reductions tell the compiler (loops over the item's
-  // tiles stay in uniform registers)
-  auto take_item = [&](int it, auto whole) {
-    const bool ok = mbar_wait(&item_full[it & 1], (it >> 1) & 1, abort_flag, p.dev_err);
+  // PERS: this warp's next item, number it; false: none is left (or a wait failed).  softmax: the
+  // softmax warps take it or leave it together, because they meet at barriers in its tiles,
+  // which a warp whose wait has failed would miss; and a warp's lanes read it together, which
+  // the reductions tell the compiler (loops over the item's tiles stay in uniform registers)
+  auto take_item = [&](int it, auto softmax) {
+    bool ok = mbar_wait(&item_full[it & 1], (it >> 1) & 1, abort_flag, p.dev_err);
+    if constexpr (decltype(softmax)::value) ok = named_bar_and(1, 32 * NSW, ok);
     const int* m = items + (it & 1) * L::ITEM;
     auto get = [&](int x) {
-      if constexpr (decltype(whole)::value) return __reduce_max_sync(0xffffffffu, x);
+      if constexpr (decltype(softmax)::value) return __reduce_max_sync(0xffffffffu, x);
       else return x;
     };
     nkt = get(ok ? m[0] : -1);
@@ -727,7 +729,6 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
         }
         const int t0 = tile_of(j) * KT;                   // MOD: the tile's first key,
         const int h0 = t0 + hf * KC;                      // ... and this thread's
-        uint32_t unseen[4] = {0, 0, 0, 0};                // MOD: keys that no row of the CTA sees
         uint32_t seen[KC / 32] = {};                      // MOD: keys that this row sees (edge)
         bool whole = true, edge = false;
         float shift = 0.f;                                // MOD: to be added to every score
@@ -749,16 +750,13 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
               tmem_ld16(tl + s * 128 + hf * KC + c, *reinterpret_cast<float(*)[16]>(&sv[c]));
             tmem_wait_ld();
           });
-          if (!whole) {   // uniform over the softmax warps
+          if (!whole) {   // read back when the values are dealt with, behind the maxima's barrier
             uint32_t* cm = colm + s * 16;
 #pragma unroll
             for (int k = 0; k < KC / 32; ++k) {
               const uint32_t w = __reduce_or_sync(0xffffffffu, seen[k]);
               if (lane == 0) cm[quarter * 4 + hf * (KC / 32) + k] = w;
             }
-            named_bar_sync(1, 32 * NSW);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
           }
         }
         const bool full_tile = MOD || __all_sync(0xffffffffu, lim >= KT - 1);   // below the diagonal
@@ -782,7 +780,8 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
           mx = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3]));
           if constexpr (MOD) mx += shift;
           if constexpr (HALVES > 1) {
-            // the row's largest: this half's and the other's
+            // the row's largest: this half's and the other's.  Every softmax warp comes past these
+            // barriers for every tile, whatever its waits and masks said
             float* hm = half_max + (L::HB > 1 ? s * 256 : 0);
             if (L::HB == 1) named_bar_sync(2, 32 * NSW);   // the last tile's have been read
             hm[hf * 128 + r] = mx;
@@ -867,10 +866,17 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
         }
         l_run = l_run * alpha + rsum;
         m_run = m_new;
-        if (MOD && (unseen[0] | unseen[1] | unseen[2] | unseen[3])) {
-          // keys that no row sees (among them tokens past the end and rejected pages): the same
-          ok = mbar_wait(&v_full[g % NS], (g / NS) & 1, abort_flag, p.dev_err) && ok;
-          zero_values(g, unseen, threadIdx.x - 64, 32 * NSW);
+        if (MOD && !whole) {
+          // keys that no row of the CTA sees (among them tokens past the end and rejected pages):
+          // the same
+          const uint32_t* cm = colm + s * 16;
+          uint32_t unseen[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) unseen[k] = ~(cm[k] | cm[4 + k] | cm[8 + k] | cm[12 + k]);
+          if (unseen[0] | unseen[1] | unseen[2] | unseen[3]) {
+            ok = mbar_wait(&v_full[g % NS], (g / NS) & 1, abort_flag, p.dev_err) && ok;
+            zero_values(g, unseen, threadIdx.x - 64, 32 * NSW);
+          }
         }
         if (!MOD && j * KT + KT > Lb) {
           // tokens past the end of the request: zero their value rows so that whatever the

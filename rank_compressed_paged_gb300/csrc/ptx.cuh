@@ -447,6 +447,20 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The same meeting point; whether x holds for every one of its threads.
+__device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bool x) {
+  __syncwarp();
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(all)
+      : "r"(id), "r"(nthreads), "r"(x ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
 
 // Host: launch `kernel` on `stream`, as a programmatic dependent of the previous kernel
 // in the stream when `pdl` is set.

@@ -1,7 +1,10 @@
-"""Barriers of the kernels, read from their sources (no GPU): a barrier that a warp may miss, or
-that its lanes reach apart, would hang the GPU, so none of these is tried out there."""
+"""Barriers of the kernels, read from their sources: one that a warp may miss, or that its lanes
+reach apart, would hang the GPU, so that is not tried out there.  On the GPU: a wait that runs
+out in some warps of a block, behind bounded waits only."""
 import os
 import re
+
+import pytest
 
 from rank_compressed_paged_gb300 import build
 
@@ -37,3 +40,60 @@ def test_aligned_barriers_join_the_lanes_of_a_warp_first():
     for name in sorted(os.listdir(build.CSRC)):      # ... and no other place has one
         if name != "ptx.cuh":
             assert not re.search(r'asm[^;]*"[^"]*\b(bar|barrier)\.(sync|red|cta|cluster)', source(name)), name
+
+
+def enclosing(text, at):
+    """Heads of the blocks around position ``at``, outermost first, and the statement there."""
+    heads, start = [], 0
+    for i in range(at):
+        if text[i] == "{":
+            heads.append(" ".join(text[start:i].split()))
+        elif text[i] == "}":
+            heads.pop()
+        if text[i] in "{};" and text[:i + 1].count("(", start) == text[:i + 1].count(")", start):
+            start = i + 1
+    return heads, " ".join(text[start:at].split())
+
+
+def test_softmax_warps_of_the_prefill_meet_whatever_their_waits_said():
+    """Waits are bounded and may fail in one warp and not in another, named barriers are neither:
+    no branch around one may hang on a wait's outcome or on what a failed wait leaves unread.
+    The tiles' number and the item are the same in all of these warps: the item by vote."""
+    text = source("prefill.cu")
+    kernel = text[text.index("prefill_kernel("):text.index("cudaError_t prepare_prefill")]
+    uniform = [r"if constexpr \(.*\)( ok =)?$", r"if \(L::HB == 1\)$", r"if \(!PERS \|\| nkt > 0\)$",
+               r"for \(int it = 0, g0 = 0;; \+\+it\)$", r"for \(int j = 0; j < nkt; \+\+j\)$",
+               r"auto take_item = .*$"]
+    calls = [m.start() for m in re.finditer(r"\bnamed_bar_\w+\(", kernel)]
+    assert len(calls) >= 4
+    for at in calls:
+        heads, statement = enclosing(kernel, at)
+        for head in heads + [statement]:
+            branch = re.search(r"\b(if|for|while|switch)\b.*", head)
+            assert branch is None or any(re.search(u, head) for u in uniform), (head, heads)
+    take = body(kernel, r"auto take_item = ")
+    assert take.index("named_bar_and(") < take.index("items +") < take.index("ok ? m[0] : -1")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("late", [0x00, 0x01, 0x80, 0x7E, 0xFF])
+def test_a_wait_that_runs_out_in_some_warps_ends_all_of_them(tmp_path, late):
+    """Eight warps that meet at a barrier per item; the wait for item 3 runs out in the warps of
+    the mask ``late`` (nothing ever arrives there), after two seconds."""
+    import ctypes
+    import subprocess
+    import torch
+    from rank_compressed_paged_gb300 import _lib
+    lib = str(tmp_path / "bounded_waits.so")
+    subprocess.run([build.nvcc(), *build.ARCH, *build.FLAGS, "-shared", "-o", lib,
+                    os.path.join(os.path.dirname(os.path.abspath(__file__)), "bounded_waits.cu")],
+                   check=True)
+    taken = torch.full((256,), -1, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run = ctypes.CDLL(lib).run
+    run.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_uint, ctypes.c_void_p, ctypes.c_void_p]
+    torch.cuda.synchronize()
+    assert run(5, 3, late, taken.data_ptr(), err.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert bool((taken == (3 if late else 5)).all()), taken
+    assert int(err) == (_lib.RCP_DEVERR_TIMEOUT if late else 0)
