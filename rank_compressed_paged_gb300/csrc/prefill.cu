@@ -317,6 +317,12 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
                                 (tok % kBlockSize) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
     }
   };
+  // A warp whose copies or MMAs may still be under way when it has nothing left to do (a wait
+  // failed somewhere) stays until they are done: this CTA's memory is another's once it has
+  // left.  n tiles' copies in all, the last NS of which may be on their way.
+  auto drain_copies = [&](uint64_t* full, int n) {
+    for (int i = max(0, n - NS); i < n; ++i) mbar_wait_drain(&full[i % NS], (i / NS) & 1);
+  };
   if (warp == 0) {
     // ------------------------------------------------------------------ key copies
     // The whole warp: lane jb < 8 resolves page jb of each tile one tile ahead and issues
@@ -332,6 +338,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
     if (!PERS && lane == 0) load_queries(0, q_full);
     bool ok = true;
     [[maybe_unused]] int nq = 0;                          // PERS: items with key tiles
+    int issued = 0;                                       // tiles whose copies are under way or done
     for (int it = 0, g0 = 0; ok; ++it) {                  // g0: tiles of the items before
       if constexpr (PERS) {
         int w = blockIdx.x;
@@ -397,12 +404,19 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
           if (ok) mbar_arrive_expect_tx(&k_full[s], nload * 2048);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);             // the byte count is armed first
+        if (ok) issued = g + 1;
         if (ok && phys >= 0)
           tma_load_2d(sm + L::ST_OFF + s * L::STAGE + lane * 2048, &kp_map, 0,
                       (phys * H + h) * kBlockSize, &k_full[s]);
       }
       g0 += nkt;
       if constexpr (!PERS) break;
+    }
+    if (lane == 0) {
+      drain_copies(k_full, issued);
+      if constexpr (!PERS) mbar_wait_drain(q_full, 0);
+      if (PERS && nq > 0) mbar_wait_drain(nq & 1 ? q_full : q_full2, ((nq - 1) >> 1) & 1);
+      if (PERS && nq > 1) mbar_wait_drain(nq & 1 ? q_full2 : q_full, ((nq - 2) >> 1) & 1);
     }
   } else if (warp == 2 + NSW) {
     // ---------------------------------------------------------------- value copies
@@ -411,6 +425,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
       if (lane == 0) {
         prefetch_tmap(&vp_map);
         bool ok = true;
+        int issued = 0;
         for (int it = 0, g0 = 0; ok; ++it) {
           if constexpr (PERS) {
             if (!take_item(it, std::false_type{})) break;
@@ -428,6 +443,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
             ok = g < NS || mbar_wait(&v_empty[s], ((g / NS) - 1) & 1, abort_flag, p.dev_err);
             if (!ok) break;
             mbar_arrive_expect_tx(&v_full[s], NG * KT * 128);
+            issued = g + 1;
             const int x = tile_of(j);
             const int64_t vrow = first + static_cast<int64_t>(MOD && x >= npt ? x - tile0 : x) * KT;
 #pragma unroll
@@ -438,6 +454,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
           g0 += nkt;
           if constexpr (!PERS) break;
         }
+        drain_copies(v_full, issued);
       }
     } else {
       // the value rank slice of each page: lane jb < 8 resolves page jb of each tile one
@@ -447,6 +464,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
       const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.bt_stride;
       const int pg0 = tile_of(0) * BPT + lane;
       int32_t nxt = (lane < BPT && nkt > 0 && page_read(pg0)) ? table[pg0] : -1;
+      int issued = 0;
       for (int j = 0; j < nkt; ++j) {
         const int s = j % NS;
         const bool mine = lane < BPT && page_read(tile_of(j) * BPT + lane);
@@ -461,6 +479,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
           if (go) mbar_arrive_expect_tx(&v_full[s], nload * NG * 2048);
         }
         if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        issued = j + 1;
         uint8_t* vst = sm + L::ST_OFF + s * L::STAGE + L::K_BYTES;
         if (phys >= 0) {
 #pragma unroll
@@ -479,6 +498,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
                         slice * RQ + kb * 64, w_full);
         mbar_wait_drain(w_full, 0);
       }
+      if (lane == 0) drain_copies(v_full, issued);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------------- MMAs
@@ -607,7 +627,8 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
         while (ok && gs < g + 3 && scores(false)) {
         }
       }
-      if (!PERS && leader) umma_commit(acc_done);
+      if (leader) umma_commit(PERS ? o_done : acc_done);
+      mbar_wait_drain(PERS ? o_done : acc_done, 0);
     }
     if (!(MOD && RECON) && lane == 0) {
       constexpr uint32_t id_s = make_idesc_f16(128, KT, false, false);
@@ -690,10 +711,8 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
           umma_f16(tmem, make_sdesc(zl + koff, 16, 1024, kSwizzle128B), bd, id_o, 1u);
         }
       }
-      if (!RECON) {
-        umma_commit(o_done);
-        mbar_wait_drain(o_done, 0);
-      }
+      if (!RECON) umma_commit(o_done);
+      mbar_wait_drain(RECON ? acc_done : o_done, 0);
     }
   } else {
     // ----------------------------------------------- softmax (one thread per query row, or

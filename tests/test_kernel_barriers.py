@@ -75,6 +75,27 @@ def test_softmax_warps_of_the_prefill_meet_whatever_their_waits_said():
     assert take.index("named_bar_and(") < take.index("items +") < take.index("ok ? m[0] : -1")
 
 
+def test_prefill_warps_stay_until_their_copies_and_products_are_done():
+    """After a failed wait too: behind its last copy or MMA each of these warps waits (with a
+    limit) for what it has under way, before the tensor memory is given back and the CTA leaves."""
+    text = source("prefill.cu")
+    kernel = text[text.index("prefill_kernel("):text.index("cudaError_t prepare_prefill")]
+    keys = body(kernel, r"if \(warp == 0\) \{")
+    values = body(kernel, r"else if \(warp == 2 \+ NSW\) \{")
+    products = body(kernel, r"else if \(warp == 1\) \{")
+    joint = body(values, r"\} else \{")
+    rebuilt = values[:values.index(joint)]
+    for code, done in ((keys, "drain_copies(k_full, issued)"), (rebuilt, "drain_copies(v_full, issued)"),
+                       (joint, "drain_copies(v_full, issued)")):
+        assert code.rindex("tma_load_2d(") < code.rindex(done)
+    assert keys.rindex("load_queries(") < keys.rindex("mbar_wait_drain(q_full")
+    mod = body(products, r"if constexpr \(MOD\) \{")
+    plain = body(products, r"if \(!\(MOD && RECON\) && lane == 0\) \{")
+    for code in (mod, plain):
+        assert code.rindex("umma_f16") < code.rindex("umma_commit(") < code.rindex("mbar_wait_drain(")
+    assert kernel.rindex("mbar_wait_drain(") < kernel.rindex("tmem_dealloc(")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("late", [0x00, 0x01, 0x80, 0x7E, 0xFF])
 def test_a_wait_that_runs_out_in_some_warps_ends_all_of_them(tmp_path, late):
