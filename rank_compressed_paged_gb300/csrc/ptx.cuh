@@ -360,16 +360,15 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 // Full cluster barrier (release / acquire): every thread of every CTA must take part.
-// (The aligned forms, which the lanes of a warp have to reach together: joined first.)
+// (Not the aligned forms: the lanes of a warp may come to it one by one.  Joining them first
+// made the reconstruction, whose producer warps end in one lane's loop, 10 us slower in a
+// prefill step of 730.)
 __device__ __forceinline__ void cluster_sync_all() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // The same meeting point without ordering any memory access.
 __device__ __forceinline__ void cluster_sync_relaxed() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 // Shared-memory address of the same variable in the CTA of cluster rank `rank`.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t local_smem, uint32_t rank) {
