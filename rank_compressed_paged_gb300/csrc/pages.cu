@@ -94,8 +94,9 @@ __global__ void __launch_bounds__(kCopyThreads)
 // request (from L2).  Slices of 128 to 256 bytes keep whole rows together.  Measured, half of
 // 64 x 8192 tokens kept: fp16 370 us (6.4 TB/s, 0.94 of the copy rate), E4M3 217 us (5.5),
 // 4-bit 146 us (4.3: a kept token's key rows are 32-byte pieces, of 64-byte memory accesses);
-// 0.6 of one 30001-token request: 68, 35 and 29 us, of which the scan of the mask and the
-// list take 7; there a window costs the latency of its loads plus the cluster's barrier.
+// 0.6 of one 30001-token request: 69, 36 and 32 us (the 4-bit one 35 with the pages out of L2),
+// of which the scan of the mask and the list take 7; there a window costs the latency of its
+// loads plus the cluster's barrier, whose ordering of memory costs 1 to 3 us of them.
 // (Slices of 64 bytes and one CTA each, the first form, took 644 us and, with all 4-bit key
 // scales in one slice, 909 us for the single request.)
 constexpr int kCmpThreads = 512;
@@ -120,13 +121,8 @@ struct CompactSmem {
   int32_t spage[kCmpPages];            // the span's pages
   int32_t dpage[kCmpPages + 1];        // pages of its destinations
   uint64_t wsum[kCmpThreads / 32];     // a warp's kept tokens, 16 bits per quarter
-  uint32_t sink[kCmpThreads / 32];
   int32_t moved;                       // first kept token of the span that moves
 };
-
-__device__ __forceinline__ uint32_t first_word(uint4 v) { return v.x; }
-__device__ __forceinline__ uint32_t first_word(uint2 v) { return v.x; }
-__device__ __forceinline__ uint32_t first_word(uint16_t v) { return v; }
 
 // Moves kept tokens first .. count - 1 of a span: token i from position s0 + src[i] to d0 + i,
 // all of them above their destination (a page whose tokens all stay is not written: it may
@@ -168,19 +164,10 @@ __device__ __forceinline__ void move_span(const Slice& sl, CompactSmem& sm, int 
         else bad = true;
       }
     }
-    // every thread of the cluster has loaded this window
-    if (CLUSTER) {
-      // the barrier's release would wait for the window before's stores, which nobody in this
-      // kernel reads; it is enough that this thread's loads have returned, which the store of
-      // a value made of them into shared memory waits for
-      uint32_t seen = 0;
-#pragma unroll
-      for (int k = 0; k < UNR; ++k) seen ^= first_word(r[k]);
-      const_cast<volatile uint32_t&>(sm.sink[threadIdx.x / 32]) = seen;
-      cluster_sync_relaxed();
-    } else {
-      __syncthreads();
-    }
+    // every thread of the cluster has loaded this window, before any of them stores it: the
+    // barrier releases and acquires, which orders other threads' stores behind these loads
+    if (CLUSTER) cluster_sync_all();
+    else __syncthreads();
 #pragma unroll
     for (int k = 0; k < UNR; ++k) {
       int i, u;

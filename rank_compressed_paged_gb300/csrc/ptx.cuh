@@ -366,10 +366,6 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The same meeting point without ordering any memory access.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
-}
 // Shared-memory address of the same variable in the CTA of cluster rank `rank`.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t local_smem, uint32_t rank) {
   uint32_t r;

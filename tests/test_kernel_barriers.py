@@ -44,6 +44,13 @@ def test_aligned_barriers_join_the_lanes_of_a_warp_first():
             assert not re.search(r'asm[^;]*"[^"]*\b(bar|barrier)\.(sync|red|cta|cluster)', source(name)), name
 
 
+def test_cluster_barriers_order_memory():
+    """Behind a cluster barrier other CTAs overwrite or read what this one loaded or stored."""
+    for name in sorted(os.listdir(build.CSRC)):
+        for form in re.findall(r"barrier\.cluster\.(?:arrive|wait)[.\w]*", source(name)):
+            assert ".release" in form or ".acquire" in form, (name, form)
+
+
 def enclosing(text, at):
     """Heads of the blocks around position ``at``, outermost first, and the statement there."""
     heads, start = [], 0
