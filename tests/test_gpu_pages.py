@@ -345,3 +345,41 @@ def test_calls_on_nothing():
     torch.cuda.synchronize()
     assert np.array_equal(raw(cache.k_pages), raw(k)) and np.array_equal(raw(cache.v_pages), raw(v))
     assert cache.read_device_error() == 0
+
+
+# ------------------------------------------------- requests of several spans of 32768 tokens
+def span_masks(lens, T, name):
+    """none of the first span moves; a destination inside a page is carried over to the second;
+    whole spans are dropped; every third token goes."""
+    rng = np.random.default_rng(21)
+    B, pos = len(lens), np.arange(T)[None]
+    if name == "second_moves":
+        keep = np.broadcast_to(pos != 32768 + 5, (B, T))
+    elif name == "carried":
+        keep = np.broadcast_to(~np.isin(pos, [3, 32000, 32766]) & (pos % 7 != 5), (B, T))
+    elif name == "late_carried":                       # the first move is the span's last token
+        keep = np.broadcast_to((pos != 32766) & ((pos < 33000) | (rng.random((B, T)) < 0.4)), (B, T))
+    elif name == "span_dropped":
+        keep = np.broadcast_to(((pos < 11) | (pos >= 32768)) & (pos != 65536), (B, T))
+    else:
+        keep = rng.random((B, T)) < 0.6
+    return keep.astype(np.uint8)
+
+
+@pytest.mark.parametrize("name", ["second_moves", "carried", "late_carried", "span_dropped", "random"])
+@pytest.mark.parametrize("pages", FORMATS)
+@pytest.mark.parametrize("beside", [0, 120])
+def test_compact_tokens_over_several_spans(pages, name, beside):
+    """Few requests (a cluster of CTAs per slice), and many short ones beside the long ones (one
+    CTA per slice)."""
+    if beside:
+        lens = [70001, 32769] + [int(x) for x in np.random.default_rng(4).integers(0, 40, beside)]
+    else:
+        lens = [32767, 32768, 32769, 70001]
+    compaction(SHAPES["tiny"], pages, lens, lambda T: span_masks(lens, T, name), seed=22)
+
+
+@pytest.mark.parametrize("pages", FORMATS)
+def test_compact_tokens_over_several_spans_main_shape(pages):
+    lens = [33007]
+    compaction(SHAPES["main"], pages, lens, lambda T: span_masks(lens, T, "late_carried"), seed=23)
