@@ -967,7 +967,9 @@ __global__ void __launch_bounds__(decode_threads<S, FMT, SKIP>(), 1)
   if (active) walk.init(p, max_len, b_first, s_first);
 
   if (!active) {
-    // no blocks for this CTA
+    // no blocks for this CTA.  Where no CTA has any, the first waits for the launch ahead (a
+    // step's append) all the same: a launch behind this one goes by this one's end
+    if (writer) griddep_wait();
   } else if (warp == 0) {
     // ------------------------------------------------------------------ copy producer
     // The whole warp looks up the block ids and valid tokens of 32 pages at a time (lane l:

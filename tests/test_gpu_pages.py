@@ -383,3 +383,38 @@ def test_compact_tokens_over_several_spans(pages, name, beside):
 def test_compact_tokens_over_several_spans_main_shape(pages):
     lens = [33007]
     compaction(SHAPES["main"], pages, lens, lambda T: span_masks(lens, T, "late_carried"), seed=23)
+
+
+@pytest.mark.parametrize("pages", FORMATS)
+@pytest.mark.parametrize("masked", [True, False])
+def test_a_step_without_visible_tokens_ends_with_its_append(pages, masked):
+    """A step of which no row sees a token (masked: by its row_begin; else by its length) still
+    appends; the page copy queued behind it takes the appended pages."""
+    import torch
+    shape = SHAPES["main"]
+    H, d = shape["num_heads"], shape["head_dim"]
+    n, B, tokens = 400, 3, 2048
+    k, v = random_pages(shape, pages, n, seed=24)
+    cache, other = new_cache(shape, pages, k, v), new_cache(shape, pages, k, v)
+    rng = np.random.default_rng(25)
+    new_k, new_v = (t(wl.fp16(rng.standard_normal((tokens, H, d)))) for _ in range(2))
+    slots = t(rng.permutation(tokens).astype(np.int64))          # blocks 0 .. 127
+    q = t(wl.fp16(rng.standard_normal((B, H, d))))
+    table = t(np.arange(3 * 9, dtype=np.int32).reshape(B, 9) + 150)
+    lens = t(np.full(B, 120 if masked else 0, np.int32))
+    mod = score_mod(dict(row_begin=np.full(B, 120))) if masked else None
+    pairs = t(np.stack([np.arange(128), 200 + np.arange(128)], 1).astype(np.int32))
+    other.append_kv(new_k, new_v, slots)
+    torch.cuda.synchronize()
+    want = [x[:128].clone() for x in (other.k_pages.view(torch.uint8), other.v_pages.view(torch.uint8))]
+    old = [t(raw(x)) for x in (k, v)]
+    got = [x.view(torch.uint8) for x in (cache.k_pages, cache.v_pages)]
+    for _ in range(5):
+        for x, o in zip(got, old):
+            x.copy_(o)
+        cache.decode_step(new_k, new_v, slots, q, table, lens, mod=mod)
+        cache.copy_blocks(pairs)
+        torch.cuda.synchronize()
+        assert cache.read_device_error() == 0
+        for x, w in zip(got, want):
+            assert torch.equal(x[:128], w) and torch.equal(x[200:328], w)

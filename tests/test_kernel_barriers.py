@@ -51,6 +51,15 @@ def test_cluster_barriers_order_memory():
             assert ".release" in form or ".acquire" in form, (name, form)
 
 
+def test_a_decode_without_pages_waits_for_the_launch_ahead():
+    """A launch may start before the one ahead of it has ended, and what comes behind it waits
+    for this one alone: its end has to mean that the one ahead has ended too."""
+    text = source("decode.cu")
+    kernel = text[text.index("decode_main_kernel("):]
+    assert "if (writer) griddep_wait();" in body(kernel, r"if \(!active\) \{")
+    assert "const bool writer = cta == 0;" in kernel
+
+
 def enclosing(text, at):
     """Heads of the blocks around position ``at``, outermost first, and the statement there."""
     heads, start = [], 0
