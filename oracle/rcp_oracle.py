@@ -519,14 +519,19 @@ def attend_mod(q, ck, cv, U_k, W_v, head_dim: int, positions, see, softcap: floa
         s = (q[:, h] @ U[h].T) @ ck[idx, h].T / np.sqrt(head_dim)        # [n][idx]
         if softcap > 0:
             s = softcap * np.tanh(s / softcap)
-        if slopes is not None:
-            s = s - float(slopes[h]) * np.abs(pos[:, None] - idx[None, :])
         v = see[:, idx]
         for i in range(n):
             w = np.nonzero(v[i])[0]
             if w.size == 0:
                 continue
-            e = np.exp(s[i, w] - s[i, w].max())
+            x = s[i, w]
+            if slopes is not None:
+                # from the distance that the bias favours: whole numbers, so that a steep bias
+                # keeps the scores of the tokens at that distance (2^60 times 3 has no room for
+                # them in 53 bits)
+                dist = np.abs(pos[i] - idx[w])
+                x = x - float(slopes[h]) * (dist - (dist.min() if slopes[h] >= 0 else dist.max()))
+            e = np.exp(x - x.max())
             p[i, h, idx[w]] = e / e.sum()
         o[:, h] = (p[:, h][:, idx] @ cv[idx]) @ W[:, h * d:(h + 1) * d]
     return o, p

@@ -119,3 +119,21 @@ def test_compaction_by_hand(pages):
         assert np.array_equal(token(k, v, j), token(kp, vp, t))
     for t in range(4, 20):
         assert np.array_equal(token(k, v, t), token(kp, vp, t))
+
+
+@pytest.mark.parametrize("slope", [-2.0 ** 60, -2.0 ** 53])
+def test_scores_decide_between_tokens_at_the_same_distance(slope):
+    """A row in the middle of a prefix whose bias leaves its two farthest tokens alone: their
+    weights are those of their scores, whatever the bias is."""
+    inp = wl.make_decode_inputs(TINY, [7], seed=10)
+    c = inp.cache
+    ck, cv = orc.gather_request(c.k_pages, c.v_pages, c.block_table[0], 7, 16)
+    see = orc.visible_tokens(3, 7, prefix=7)[None]
+    H = inp.q.shape[1]
+    _, p = orc.attend_mod(inp.q, ck, cv, inp.U_k, inp.W_v, inp.q.shape[2], [3], see, 0.0, [slope] * H)
+    for h in range(H):
+        qt = inp.q[0, h].astype(np.float64) @ np.asarray(inp.U_k[h], np.float64).T
+        s = [float(qt @ np.asarray(ck[t, h], np.float64)) / math.sqrt(inp.q.shape[2]) for t in (0, 6)]
+        first = 1 / (1 + math.exp(s[1] - s[0]))
+        np.testing.assert_allclose(p[0, h], [first, 0, 0, 0, 0, 0, 1 - first], rtol=0, atol=1e-12)
+        assert abs(first - 0.5) > 1e-3
