@@ -33,6 +33,14 @@ __device__ __forceinline__ int32_t view_begin(const AttnParams& p, int64_t row, 
 __device__ __forceinline__ int32_t bias_origin(RowView v, int32_t pos) {
   return (v.lo <= pos || pos < v.pfx) ? pos : v.pfx - 1;
 }
+// Distance of the farthest token that the row sees from that position: what a bias that grows
+// with the distance is measured from in its turn (the prefill).
+__device__ __forceinline__ int32_t bias_reach(RowView v, int32_t pos, int32_t org) {
+  const int32_t first = v.pfx > 0 ? 0 : v.lo;
+  const int32_t last = v.lo <= pos && pos >= v.pfx ? pos : v.pfx - 1;
+  const int32_t a = org - first, b = last - org;
+  return a > b ? a : b;
+}
 
 // A prefill request's key tiles (KT keys) that some of its rows sees: those of the prefix and
 // those from the least first token of any row on, from the plan's (prefix, least first token).
@@ -113,17 +121,18 @@ __device__ __forceinline__ uint32_t column_bits(int32_t a, int32_t b, int32_t c0
 }
 
 // A prefill row's modifications: what it sees, where its bias starts from (log2 units per
-// token), and whether one of its warp's scores has passed the range of the cap's polynomial.
+// token; reach: the distance at which it is zero), and whether one of its warp's scores has passed the range of the cap's polynomial.
 struct RowMod {
   RowView view;
   int32_t pos, org;
-  float slope2;
+  float slope2, reach;
   bool far;
   CapNear near;
   __device__ __forceinline__ RowMod(const AttnParams& p, int head, bool row_ok, int64_t row,
                                     int32_t pos_, int32_t pfx)
       : view{pfx, row_ok ? view_begin(p, row, pos_) : 0}, pos(pos_), org(bias_origin(view, pos_)),
-        slope2(p.slopes ? p.slopes[head] * 1.44269504f : 0.f), far(false),
+        slope2(p.slopes ? p.slopes[head] * 1.44269504f : 0.f),
+        reach(slope2 < 0.f ? static_cast<float>(bias_reach(view, pos, org)) : 0.f), far(false),
         near(p.cap2, p.inv_cap2) {
     if (!row_ok) near.w_near = INFINITY;   // a row outside the chunk has no say in the form
   }
@@ -175,16 +184,20 @@ __device__ __forceinline__ float modify_scores(float (&sv)[KC], const AttnParams
     }
   }
   if (p.slopes) {
-    if (__all_sync(0xffffffffu, h0 + KC - 1 <= rm.org)) {
-      // every key at or before the origin: slope (t - org), the part they share kept apart
-      shift = rm.slope2 * static_cast<float>(h0 - rm.org);
+    // Every key at or before the origin: slope (t - org), the part they share kept apart.  The
+    // row's maximum then holds that part, and the weights are off by up to its rounding (2^-4
+    // below 2^20; past it they could leave fp16's range).  A bias that grows with the distance
+    // is largest where that part is: no key is worked out so.
+    const float part = rm.slope2 * static_cast<float>(h0 - rm.org);
+    if (__all_sync(0xffffffffu, h0 + KC - 1 <= rm.org && part <= 0.f && part > -1048576.f)) {
+      shift = part;
 #pragma unroll
       for (int c = 0; c < KC; ++c) sv[c] = fmaf(rm.slope2, static_cast<float>(c), sv[c]);
     } else {
       const float d0 = static_cast<float>(rm.org - h0);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
-        sv[c] = fmaf(-rm.slope2, fabsf(d0 - static_cast<float>(c)), sv[c]);
+        sv[c] = fmaf(-rm.slope2, fabsf(d0 - static_cast<float>(c)) - rm.reach, sv[c]);
     }
   }
   if (edge) {

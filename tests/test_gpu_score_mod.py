@@ -694,3 +694,35 @@ def test_calls_without_requests_or_rows(shape_name, pages):
     assert cache.prefill_attn(q, cu, table, lens, mod=mod).shape == q.shape
     torch.cuda.synchronize()
     assert cache.read_device_error() == 0
+
+
+def steep_slopes(shape):
+    """Biases that leave one token of a row any weight: its nearest, or (negative) its farthest."""
+    return [(1.0, -1.0)[h % 2] * 2.0 ** (9, 14, 20, 27, 34, 60)[h // 2 % 6]
+            for h in range(shape["num_heads"])]
+
+
+@pytest.mark.parametrize("extra", [dict(), dict(window=77), dict(window=50, prefix_lens=7, softcap=11.0)])
+@pytest.mark.parametrize("shape_name,pages", [("main", "fp16"), ("main", "int4"), ("tiny", "fp8_e4m3")])
+def test_steep_biases(shape_name, pages, extra):
+    """Up to the largest magnitude allowed: the row is the value of one token, exactly weighted."""
+    import torch
+    for chunked in (False, True):
+        inp = prefill_inputs(shape_name, pages) if chunked else decode_inputs(shape_name, pages)
+        mod = dict(alibi_slopes=steep_slopes(inp.shape), **extra)
+        if "prefix_lens" in mod:
+            mod["prefix_lens"] = np.full(len(PRIOR if chunked else LENS), mod["prefix_lens"])
+        if chunked:
+            ref = oracle_prefill(inp, shape_name, pages, f"steep{len(extra)}", mod)
+            for variant in ("rank", "reconstruct"):
+                cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+                out = cache.prefill_attn(t(inp.q), t(inp.cu_chunk_lens), t(inp.cache.block_table),
+                                         t(inp.seq_lens_after), variant=variant, mod=score_mod(mod))
+                assert_within(out.cpu().numpy(), ref, f"prefill {variant}")
+        else:
+            cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.k, inp.v)
+            out = cache.decode_attn(t(inp.q), t(inp.cache.block_table), t(inp.cache.seq_lens),
+                                    mod=score_mod(mod))
+            assert_within(out.cpu().numpy(), oracle_decode(inp, pages, mod), "decode")
+        torch.cuda.synchronize()
+        assert cache.read_device_error() == 0
