@@ -184,6 +184,11 @@ class ScoreMod:
         if not -2**31 <= self.window < 2**31:
             raise ValueError(f"window must fit 32 bits, got {self.window}")
 
+    def modifies(self) -> bool:
+        """Whether a call with it differs from the plain one."""
+        return (self.softcap != 0 or self.window != 0 or self.alibi_slopes is not None
+                or self.prefix_lens is not None or self.row_begin is not None)
+
     def _args(self):
         def at(x):
             return None if x is None else _ptr(x)
@@ -463,11 +468,12 @@ class PagedCoeffCache:
         return out
 
     def _prefill_variant(self, variant: str, rows: int, B: int, mod=None) -> str:
-        if variant == "auto" and mod is not None:
-            # one 128-row tile is 128 rank-space CTAs, one wave of the SMs; measured with capped
-            # scores, rank space against reconstruction: one request of up to 8 rows 37 / 42 us
-            # behind 777 tokens, 91 / 112 behind 4096, 613 / 762 behind 32768; four of them
-            # 120 / 57, 337 / 197 and 2348 / 1439
+        if variant == "auto" and isinstance(mod, ScoreMod) and mod.modifies():
+            # one 128-row tile is 128 rank-space CTAs, one wave of the SMs; measured, rank space
+            # against reconstruction in us, 1 to 128 rows of one request: capped behind 777 tokens
+            # 36-39 / 39-41, behind 4096 85-96 / 100-111, behind 32768 512-594 / 628-722, a window
+            # of 1024 35-37 / 43-44; two requests 64-66 / 46-47, 178-182 / 137-140, 1136-1175 /
+            # 877-907 and 62-64 / 44-46 (the small shape: within 8 us of each other, or 8 %)
             variant = "rank" if self.page_format == "fp16" and B == 1 and rows <= 128 else "reconstruct"
         if variant == "auto":
             variant = "reconstruct" if (self.page_format != "fp16" or
@@ -506,7 +512,9 @@ class PagedCoeffCache:
         RECONSTRUCT_MIN_CHUNK rows.  The multiply-add count favours reconstruction above
         prefill_crossover_rows() (147 for R = 1024, d = 128); measured on GB300 it is the
         faster variant from 16-row chunks on (priors 4096 to 32768), because a chunk shorter
-        than one 128-row tile costs the rank-space kernel a whole tile per R slice."""
+        than one 128-row tile costs the rank-space kernel a whole tile per R slice.  Under a mod
+        that modifies anything "auto" is rank for one request of up to 128 rows on fp16 pages,
+        else reconstruct."""
         import torch
         if out is None:
             out = torch.empty_like(q)

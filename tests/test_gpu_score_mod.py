@@ -726,3 +726,17 @@ def test_steep_biases(shape_name, pages, extra):
             assert_within(out.cpu().numpy(), oracle_decode(inp, pages, mod), "decode")
         torch.cuda.synchronize()
         assert cache.read_device_error() == 0
+
+
+@pytest.mark.parametrize("prior,chunk", [([500], [100]), ([90, 300, 40, 7], [8, 3, 5, 9])])
+def test_auto_variant_without_effective_modifications_is_the_plain_call(prior, chunk):
+    """Bit for bit, at sizes where the plain rule and the one under modifications differ."""
+    import torch
+    shape = SHAPES["main"]
+    inp = wl.make_prefill_inputs(shape, prior, chunk, seed=351, fill=0.5)
+    c = inp.cache
+    cache = cache_of("fp16", shape, inp.U_k, inp.W_v, c.k_pages, c.v_pages)
+    args = (t(inp.q), t(inp.cu_chunk_lens), t(c.block_table), t(inp.seq_lens_after))
+    plain, got = cache.prefill_attn(*args), cache.prefill_attn(*args, mod=score_mod({}))
+    torch.cuda.synchronize()
+    assert torch.equal(plain.view(torch.int16), got.view(torch.int16))

@@ -194,3 +194,24 @@ def test_compact_tensors_are_checked():
                       (dict(seq_lens=torch.zeros(3, dtype=torch.int64)), "int32")):
         with pytest.raises(ValueError, match=match):
             rcp._validate_compact(CPU, **args(**kw))
+
+
+def test_a_mod_that_modifies_nothing_leaves_the_variant_to_the_plain_rule():
+    for mod, modifies in ((ScoreMod(), False), (ScoreMod(softcap=2.0), True), (ScoreMod(window=1), True),
+                          (ScoreMod(alibi_slopes=torch.zeros(4)), True),
+                          (ScoreMod(prefix_lens=torch.zeros(1, dtype=torch.int32)), True),
+                          (ScoreMod(row_begin=torch.zeros(1, dtype=torch.int32)), True),
+                          # refused by the call itself: not the plain one
+                          (ScoreMod(softcap=float("nan")), True), (ScoreMod(window=-1), True)):
+        assert mod.modifies() is modifies
+    cache = object.__new__(rcp.PagedCoeffCache)
+    for pages in ("fp16", "int4"):
+        cache.page_format = pages
+        for rows, B in ((1, 1), (8, 1), (128, 1), (129, 1), (8, 4), (64, 4), (500, 4), (0, 0)):
+            plain = cache._prefill_variant("auto", rows, B)
+            assert cache._prefill_variant("auto", rows, B, ScoreMod()) == plain, (pages, rows, B)
+            for v in ("rank", "reconstruct"):
+                assert cache._prefill_variant(v, rows, B, ScoreMod(window=3)) == v
+    cache.page_format = "fp16"
+    assert cache._prefill_variant("auto", 128, 1, ScoreMod(window=3)) == "rank"
+    assert cache._prefill_variant("auto", 8, 2, ScoreMod(window=3)) == "reconstruct"
