@@ -178,21 +178,26 @@ class ScoreMod:
                  prefix_lens=None, row_begin=None):
         self.softcap = float(softcap)
         self.alibi_slopes = alibi_slopes
-        self.window = int(window)
+        self.window = window
         self.prefix_lens = prefix_lens
         self.row_begin = row_begin
-        if not -2**31 <= self.window < 2**31:
-            raise ValueError(f"window must fit 32 bits, got {self.window}")
+        self._window()
 
     def modifies(self) -> bool:
         """Whether a call with it differs from the plain one."""
         return (self.softcap != 0 or self.window != 0 or self.alibi_slopes is not None
                 or self.prefix_lens is not None or self.row_begin is not None)
 
+    def _window(self) -> int:
+        w = int(self.window)
+        if w != self.window or not -2**31 <= w < 2**31:   # ctypes would keep the low 32 bits
+            raise ValueError(f"window must be a whole number of 32 bits, got {self.window}")
+        return w
+
     def _args(self):
         def at(x):
             return None if x is None else _ptr(x)
-        return _lib.ScoreModArgs(self.softcap, self.window, at(self.alibi_slopes),
+        return _lib.ScoreModArgs(self.softcap, self._window(), at(self.alibi_slopes),
                                  at(self.prefix_lens), at(self.row_begin))
 
 

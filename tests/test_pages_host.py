@@ -215,3 +215,16 @@ def test_a_mod_that_modifies_nothing_leaves_the_variant_to_the_plain_rule():
     cache.page_format = "fp16"
     assert cache._prefill_variant("auto", 128, 1, ScoreMod(window=3)) == "rank"
     assert cache._prefill_variant("auto", 8, 2, ScoreMod(window=3)) == "reconstruct"
+
+
+def test_a_window_that_does_not_fit_is_refused_whenever_it_was_set():
+    for bad in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 5, 2.5, float("nan")):
+        with pytest.raises(ValueError):
+            ScoreMod(window=bad)
+        mod = ScoreMod(window=7)
+        mod.window = bad
+        with pytest.raises(ValueError):
+            mod._args()
+    mod = ScoreMod(window=7)
+    mod.window = 2 ** 31 - 1
+    assert mod._args().window == 2 ** 31 - 1 and ScoreMod(window=4096.0)._args().window == 4096
