@@ -205,7 +205,7 @@ class PagedCoeffCache:
     """Paged low-rank coefficient cache on one GPU.
 
     Owns (as torch tensors) the K pages [num_blocks][H][16][r_k], V pages
-    [num_blocks][16][R], the factors, a device error word and a reusable workspace; the
+    [num_blocks][16][R], the factors, a device error word; the
     library handle borrows their pointers.  page_format "fp16" stores fp16 coefficients,
     "fp8_e4m3" stores E4M3 codes (uint8 tensors), "int4" stores 4-bit codes with fp16
     scales as raw bytes (K pages [num_blocks][int4_page_bytes()[0]], V pages
@@ -253,7 +253,6 @@ class PagedCoeffCache:
         self.k_pages = k_pages
         self.v_pages = v_pages
         self.dev_error = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._ws = {}         # by stream
         self._ws_bytes = {}
         self._cfg = _lib.CacheConfig(num_heads, head_dim, rank_k, rank_v, BLOCK_SIZE,
                                      self.num_blocks, fmt)
@@ -346,21 +345,23 @@ class PagedCoeffCache:
         return need
 
     def workspace(self, rows: int, need: int | None = None, stream=None):
-        """Scratch for a call of ``rows`` query rows (or of ``need`` bytes) on ``stream``, reused
-        by the stream's later calls.  Calls on two streams may overlap and get one each; a call
-        that is captured gets one from its graph's memory, which no other graph or call uses."""
+        """Scratch for a call of ``rows`` query rows (or of ``need`` bytes) on ``stream``, from
+        torch's allocator: a call that is given none takes one and gives it back, which hands its
+        memory to nothing but later work of that stream (of the graph, where it is captured).
+        Calls on two streams may overlap and have one each; none is kept between calls."""
         import torch
         if stream is not None and stream != torch.cuda.current_stream():
             with torch.cuda.stream(stream):
                 return self.workspace(rows, need)
         need = self.workspace_bytes(rows) if need is None else need
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
-        key = _stream()
-        ws = self._ws.get(key)
-        if ws is None or ws.numel() < need:
-            ws = self._ws[key] = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return ws
+        return torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def _scratch(self, workspace, rows: int, stream):
+        """The caller's workspace, checked, or one for this call."""
+        if workspace is None:
+            return self.workspace(rows, stream=stream)
+        _validate_workspace(self.device, workspace)
+        return workspace
 
     def reconstruct_workspace_bytes(self, rows: int, batch: int, max_blocks_per_seq: int) -> int:
         n = ctypes.c_size_t()
@@ -421,8 +422,7 @@ class PagedCoeffCache:
             out = torch.empty_like(q)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
-        ws = self.workspace(B, stream=stream) if workspace is None else workspace
-        _validate_workspace(self.device, ws)
+        ws = self._scratch(workspace, B, stream)
         if mod is not None:
             self._decode_mod(mod, None, q, block_table, seq_lens, out, ws, stream)
             return out
@@ -444,8 +444,7 @@ class PagedCoeffCache:
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
         if page_kept is not None:
             _need("page_kept", page_kept, torch.uint8, tuple(block_table.shape), self.device)
-        ws = self.workspace(B, stream=stream) if workspace is None else workspace
-        _validate_workspace(self.device, ws)
+        ws = self._scratch(workspace, B, stream)
         _lib.check("rcp_decode_attn_sparse", self._lib.rcp_decode_attn_sparse(
             self._h, _ptr(q), _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), B,
             float(skip_threshold), _ptr(page_kept) if page_kept is not None else None,
@@ -461,8 +460,7 @@ class PagedCoeffCache:
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         _validate_append(self.device, H, d, k, v, slot_mapping)
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
-        ws = self.workspace(B, stream=stream) if workspace is None else workspace
-        _validate_workspace(self.device, ws)
+        ws = self._scratch(workspace, B, stream)
         if mod is not None:
             self._decode_mod(mod, (k, v, slot_mapping), q, block_table, seq_lens, out, ws, stream)
             return out
@@ -487,10 +485,10 @@ class PagedCoeffCache:
             raise ValueError(f"unknown prefill variant {variant!r}")
         return variant
 
-    def _prefill_workspace(self, variant: str, rows: int, B: int, mb: int, stream):
+    def _prefill_scratch(self, workspace, variant: str, rows: int, B: int, mb: int, stream):
         # quantized pages are widened into the workspace first (both variants)
-        if variant == "rank" and self.page_format == "fp16":
-            return self.workspace(rows, stream=stream)
+        if workspace is not None or (variant == "rank" and self.page_format == "fp16"):
+            return self._scratch(workspace, rows, stream)
         return self.workspace(rows, self.reconstruct_workspace_bytes(rows, B, mb), stream)
 
     def _prefill_mod(self, mod, app, q, cu_chunk_lens, block_table, seq_lens, out, ws, stream,
@@ -528,10 +526,8 @@ class PagedCoeffCache:
                                     out)
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B, mod)
-        ws = (self._prefill_workspace(variant, rows, B, mb, stream) if workspace is None
-              else workspace)
+        ws = self._prefill_scratch(workspace, variant, rows, B, mb, stream)
         if mod is not None:
-            _validate_workspace(self.device, ws)
             self._prefill_mod(mod, None, q, cu_chunk_lens, block_table, seq_lens, out, ws, stream,
                               variant)
             return out
@@ -539,7 +535,6 @@ class PagedCoeffCache:
             fn, name = self._lib.rcp_prefill_attn, "rcp_prefill_attn"
         else:
             fn, name = self._lib.rcp_prefill_attn_reconstruct, "rcp_prefill_attn_reconstruct"
-        _validate_workspace(self.device, ws)
         _lib.check(name, fn(
             self._h, _ptr(q), _ptr(cu_chunk_lens), rows, _ptr(block_table), mb, _ptr(seq_lens), B,
             _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
@@ -559,9 +554,7 @@ class PagedCoeffCache:
                                     out)
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B, mod)
-        ws = (self._prefill_workspace(variant, rows, B, mb, stream) if workspace is None
-              else workspace)
-        _validate_workspace(self.device, ws)
+        ws = self._prefill_scratch(workspace, variant, rows, B, mb, stream)
         if mod is not None:
             self._prefill_mod(mod, (k, v, slot_mapping), q, cu_chunk_lens, block_table, seq_lens,
                               out, ws, stream, variant)

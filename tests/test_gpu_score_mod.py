@@ -740,3 +740,23 @@ def test_auto_variant_without_effective_modifications_is_the_plain_call(prior, c
     plain, got = cache.prefill_attn(*args), cache.prefill_attn(*args, mod=score_mod({}))
     torch.cuda.synchronize()
     assert torch.equal(plain.view(torch.int16), got.view(torch.int16))
+
+
+def test_calls_keep_no_workspace():
+    """Calls without a workspace of the caller's, plain and modified, on several streams: the
+    allocator has all of their scratch back."""
+    import torch
+    shape, cache = stream_cache("main", "fp8_e4m3")
+    jobs = stream_jobs(cache, shape, 4)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for s in [None] + [torch.cuda.Stream() for _ in range(3)]:
+        for call, out in jobs:
+            call(s, out)
+    q = torch.zeros((2, shape["num_heads"], shape["head_dim"]), dtype=torch.float16, device="cuda")
+    table, lens = t(np.zeros((2, 3), np.int32)), t(np.full(2, 40, np.int32))
+    cache.decode_attn(q, table, lens)
+    del q, table, lens
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
+    assert cache.read_device_error() == 0
