@@ -152,6 +152,16 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _empty_like(x, stream):
+    """A result of a call on ``stream``: its memory is that stream's, because other streams' may
+    still be read or written by what was queued there before it was freed."""
+    import torch
+    if stream is None:
+        return torch.empty_like(x)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x)
+
+
 def int4_page_bytes(num_heads: int, rank_k: int, rank_v: int):
     """Bytes of one 4-bit K page and one V page: the codes (two per byte), then the fp16
     scales (one per key row of a head, one per 64 value coefficients of a token)."""
@@ -322,9 +332,8 @@ class PagedCoeffCache:
         move to the front of the request's pages.  keep: [B][max_blocks * 16] uint8.  Returns
         the new lengths [B] int32 (``new_lens``, which must not be ``seq_lens``); the pages past
         them may then be freed."""
-        import torch
         if new_lens is None:
-            new_lens = torch.empty_like(seq_lens)
+            new_lens = _empty_like(seq_lens, stream)
         B = _validate_compact(self.device, block_table, seq_lens, keep, new_lens)
         _on_current(self.device)
         _lib.check("rcp_compact_tokens", self._lib.rcp_compact_tokens(
@@ -417,9 +426,8 @@ class PagedCoeffCache:
                     mod=None):
         """q: [B][H][d] fp16; block_table: [B][max_blocks] int32; seq_lens: [B] int32; mod: None
         or a ScoreMod."""
-        import torch
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
         ws = self._scratch(workspace, B, stream)
@@ -439,7 +447,7 @@ class PagedCoeffCache:
         or a [B][max_blocks] uint8 tensor that receives 1 / 0 per page read / left out."""
         import torch
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
         if page_kept is not None:
@@ -454,9 +462,8 @@ class PagedCoeffCache:
     def decode_step(self, k, v, slot_mapping, q, block_table, seq_lens, out=None, workspace=None,
                     stream=None, mod=None):
         """append_kv(k, v, slot_mapping) then decode_attn(q, ..., mod=mod), queued as one step."""
-        import torch
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         _validate_append(self.device, H, d, k, v, slot_mapping)
         B = _validate_decode(self.device, H, d, q, block_table, seq_lens, out)
@@ -518,9 +525,8 @@ class PagedCoeffCache:
         than one 128-row tile costs the rank-space kernel a whole tile per R slice.  Under a mod
         that modifies anything "auto" is rank for one request of up to 128 rows on fp16 pages,
         else reconstruct."""
-        import torch
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         rows, B = _validate_prefill(self.device, H, d, q, cu_chunk_lens, block_table, seq_lens,
                                     out)
@@ -545,9 +551,8 @@ class PagedCoeffCache:
         """append_kv(k, v, slot_mapping) then prefill_attn(q, cu_chunk_lens, ..., mod=mod), queued
         as one step (the chunk's query projection shares the append's launch).  Arguments and
         variant choice as the two calls."""
-        import torch
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         H, d = self.shape["num_heads"], self.shape["head_dim"]
         T = _validate_append(self.device, H, d, k, v, slot_mapping)
         rows, B = _validate_prefill(self.device, H, d, q, cu_chunk_lens, block_table, seq_lens,

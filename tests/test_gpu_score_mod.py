@@ -760,3 +760,38 @@ def test_calls_keep_no_workspace():
     torch.cuda.synchronize()
     assert torch.cuda.memory_allocated() == before
     assert cache.read_device_error() == 0
+
+
+def test_results_on_another_stream_take_that_streams_memory():
+    """Memory freed on the current stream may still be in use there when a call on another
+    stream writes its result."""
+    import torch
+    shape, cache = stream_cache("main", "fp16")
+    H, d = shape["num_heads"], shape["head_dim"]
+    B, n, mb = 24, 96, 7
+    q = torch.zeros((n, H, d), dtype=torch.float16, device="cuda")
+    table, lens = t(np.zeros((B, mb), np.int32)), t(np.full(B, 100, np.int32))
+    cu, keep = t(np.arange(B + 1, dtype=np.int32) * 4), t(np.ones((B, mb * 16), np.uint8))
+    mod = score_mod(dict(window=9))
+    slots = t(np.full(B, -1, np.int64))
+    kv = torch.zeros((B, H, d), dtype=torch.float16, device="cuda")
+    side = torch.cuda.Stream()
+    calls = {
+        "decode": (q[:B], lambda: cache.decode_attn(q[:B], table, lens, stream=side)),
+        "modified decode": (q[:B], lambda: cache.decode_attn(q[:B], table, lens, stream=side, mod=mod)),
+        "sparse": (q[:B], lambda: cache.decode_attn_sparse(q[:B], table, lens, 2 ** -8, stream=side)),
+        "step": (q[:B], lambda: cache.decode_step(kv, kv, slots, q[:B], table, lens, stream=side)),
+        "prefill": (q, lambda: cache.prefill_attn(q, cu, table, lens, stream=side, mod=mod)),
+        "prefill step": (q, lambda: cache.prefill_step(kv, kv, slots, q, cu, table, lens, stream=side)),
+        "compaction": (lens, lambda: cache.compact_tokens(table, lens, keep, stream=side)),
+    }
+    torch.cuda.synchronize()
+    for name, (like, call) in calls.items():
+        freed = torch.empty_like(like)
+        at, size = freed.data_ptr(), freed.numel() * freed.element_size()
+        del freed
+        out = call()
+        assert not at - size < out.data_ptr() < at + size, name
+        del out
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
