@@ -73,9 +73,9 @@ struct TileMap {
 
 // cap2 tanh(x / cap2) of a pair of scores, log2 units, for the prefill, where a row meets 128
 // of them per tile and the FMA pipe sets the pace: six operations per score.  Scores up to 0.7
-// of the cap take a polynomial: with u = x / cap2 and v = u^2, tanh(u) / u = 1 + v q(v), q the
-// least-maximum fit of degree 3 on v in [0, 0.49] (relative error 3.2e-7, absolute 2.7e-7 of
-// the cap).  CapNear holds its coefficients in powers of x^2, c_k / cap2^(2k), within fp32 for
+// of the cap take a polynomial: with u = x / cap2 and v = u^2, tanh(u) / u = 1 + v q(v), q a fit
+// of degree 3 on v in [0, 0.49] (relative error 3.8e-7, in fp32 arithmetic 4.5e-7; absolute
+// 2.7e-7 of the cap).  CapNear holds its coefficients in powers of x^2, c_k / cap2^(2k), within fp32 for
 // every cap allowed.  wmax collects the largest x^2; the caller takes cap_far if it passed
 // w_near = (0.7 cap2)^2.
 struct CapNear {
