@@ -393,7 +393,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Named barrier over a subset of warps (id 1..15).
 __device__ __forceinline__ float fast_rcp(float x) {   // relative error about 2^-23; inf gives 0
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -436,6 +435,7 @@ __device__ __forceinline__ float2 sub_f32x2(float2 a, float2 b) {
   return *reinterpret_cast<const float2*>(&d);
 }
 
+// Named barrier over a subset of warps (id 1..15).
 // (bar.sync is the aligned form, which the lanes of a warp have to reach together: joined first,
 // because lanes part before it where one of them stores or each polls an mbarrier.)
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
