@@ -795,3 +795,52 @@ def test_results_on_another_stream_take_that_streams_memory():
         del out
     torch.cuda.synchronize()
     assert cache.read_device_error() == 0
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("name", sorted(set(prefill_mods(SHAPES["main"])) - {"all", "docs", "prefix_bias"}))
+def test_prefill_on_4_bit_pages_at_the_main_shape(name, variant):
+    """The masks that the list above leaves to the small shape."""
+    test_prefill_matches_oracle("main", "int4", name, variant)
+
+
+_long = {}
+
+
+def long_prefill(pages):
+    """Two chunks behind thousands of tokens, coefficients as given."""
+    if pages not in _long:
+        shape = SHAPES["main"]
+        inp = wl.make_prefill_inputs(shape, [5003, 2100], [139, 9], seed=361)
+        rng = np.random.default_rng(362)
+        c = inp.cache
+        kp, vp = (wl.fp16(rng.standard_normal(x.shape)) for x in (c.k_pages, c.v_pages))
+        inp.q = wl.fp16(inp.q.astype(np.float64) * 4)
+        inp.kp, inp.vp = encode(pages, kp, vp)
+        _long[pages] = inp
+    return _long[pages]
+
+
+@pytest.mark.parametrize("variant", ["rank", "reconstruct"])
+@pytest.mark.parametrize("extra", [dict(), dict(window=2500, prefix_lens=[300, 40], softcap=20.0)])
+@pytest.mark.parametrize("pages", ["fp16", "int4"])
+def test_prefill_bias_behind_thousands_of_tokens(pages, extra, variant):
+    """Gentle and ordinary biases of either sign: a tile's terms stay below 2^8 where weights are
+    not zero, of which fp32 keeps 2^-16."""
+    import torch
+    inp = long_prefill(pages)
+    H = inp.shape["num_heads"]
+    slopes = [(2.0 ** (-8 * (h + 1) / H), 2.0 ** -10, -2.0 ** -10, -2.0 ** -8)[h % 4] for h in range(H)]
+    mod = dict(alibi_slopes=slopes, **extra)
+    key = ("long", pages, len(extra))
+    if key not in _ref_cache:
+        kk, vv = values(pages, inp.shape, inp.kp, inp.vp, True)
+        _ref_cache[key] = (*orc.prefill_attn_mod(
+            inp.q, inp.cu_chunk_lens, kk, vv, inp.U_k, inp.W_v, inp.cache.block_table,
+            inp.seq_lens_after, magnitudes=True, **mod), int(max(inp.seq_lens_after)))
+    cache = cache_of(pages, inp.shape, inp.U_k, inp.W_v, inp.kp, inp.vp)
+    out = cache.prefill_attn(t(inp.q), t(inp.cu_chunk_lens), t(inp.cache.block_table),
+                             t(inp.seq_lens_after), variant=variant, mod=score_mod(mod))
+    torch.cuda.synchronize()
+    assert cache.read_device_error() == 0
+    assert_within(out.cpu().numpy(), _ref_cache[key], f"long {pages} {variant}")
