@@ -950,6 +950,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
 #pragma unroll 1
           for (int c = hf * (D / HALVES); c < (hf + 1) * (D / HALVES); c += 16) {
             float v[16];
+            __syncwarp();   // lanes past the chunk have not stored
             tmem_ld16(tl + 256 + c, v);
             tmem_wait_ld();
             uint32_t w8[8];
@@ -1055,6 +1056,7 @@ __global__ void __launch_bounds__(PfWarps<MOD>::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float v[16];
+          __syncwarp();   // lanes past the chunk have not stored
           tmem_ld16(tl + c, v);
           tmem_wait_ld();
           uint32_t w8[8];

@@ -60,6 +60,19 @@ def test_a_decode_without_pages_waits_for_the_launch_ahead():
     assert "const bool writer = cta == 0;" in kernel
 
 
+def test_tensor_memory_loads_join_the_lanes_of_a_warp_behind_a_lanes_own_store():
+    """tcgen05.ld is a warp's, not a lane's: where rows of the chunk alone are stored in a loop, its
+    next load comes behind lanes that parted."""
+    text = source("prefill.cu")
+    loops = 0
+    for m in re.finditer(r"for \(int c = [^{]*c \+= 16\) \{", text):
+        code = body(text[m.start():], r"for \(")
+        if "tmem_ld16(" in code and ("if (store)" in code or "if (i0 + r < n)" in code):
+            loops += 1
+            assert "__syncwarp();" in code.split("tmem_ld16(")[0]
+    assert loops == 2
+
+
 def enclosing(text, at):
     """Heads of the blocks around position ``at``, outermost first, and the statement there."""
     heads, start = [], 0
