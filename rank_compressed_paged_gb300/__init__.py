@@ -286,6 +286,9 @@ class PagedCoeffCache:
         return [ids[i] for i in range(n)]
 
     def free_blocks(self, ids) -> None:
+        """Takes one reference from each block, and returns it to the pool with its last.  A block
+        listed twice is refused, whatever references it has: sequences that share pages are
+        freed in a call each."""
         _lib.check("rcp_free_blocks", self._lib.rcp_free_blocks(self._h, len(ids), _ids(ids)))
 
     def num_free_blocks(self) -> int:
