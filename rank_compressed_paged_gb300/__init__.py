@@ -215,13 +215,12 @@ class PagedCoeffCache:
     """Paged low-rank coefficient cache on one GPU.
 
     Owns (as torch tensors) the K pages [num_blocks][H][16][r_k], V pages
-    [num_blocks][16][R], the factors, a device error word; the
+    [num_blocks][16][R], the factors and a device error word; the
     library handle borrows their pointers.  page_format "fp16" stores fp16 coefficients,
     "fp8_e4m3" stores E4M3 codes (uint8 tensors), "int4" stores 4-bit codes with fp16
     scales as raw bytes (K pages [num_blocks][int4_page_bytes()[0]], V pages
     [num_blocks][int4_page_bytes()[1]], uint8).  A prefill on quantized pages first widens
-    the pages it reads to fp16 in the workspace (the "auto" variant reconstructs); they have
-    no block-sparse decode.
+    the pages it reads to fp16 in the workspace (the "auto" variant reconstructs).
     """
 
     def __init__(self, num_heads: int, head_dim: int, rank_k: int, rank_v: int,
