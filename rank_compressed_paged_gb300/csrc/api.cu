@@ -446,7 +446,7 @@ rcp_status beam_plan(int32_t batch, int32_t beams, int32_t vocab, int32_t dtype,
   if (beams > rcp::kMaxBeams || vocab > rcp::kMaxVocab) return RCP_ERR_UNSUPPORTED;
   const int64_t rows = static_cast<int64_t>(batch) * beams;
   const int vec = dtype == RCP_LOGITS_FP32 ? 4 : 8;
-  const int64_t row_words = (static_cast<int64_t>(vocab) + 2 * (vec - 1)) / vec;   // unaligned ends
+  const int64_t row_words = (static_cast<int64_t>(vocab) + vec - 1) / vec;
   // segments as large as a CTA takes, or while that leaves SMs without one, halves of them down to
   // a sub-block per warp
   constexpr int kWarps = rcp::kBeamScanThreads / 32;

@@ -4,7 +4,7 @@
 //     total(i, t) = scores[i] + x[i][t] - M_i - log sum_u exp(x[i][u] - M_i),  M_i = max_u x[i][u]
 //
 // Two launches.  The scan reads the logits once: a CTA takes a segment of one row, a warp a part
-// of it in sub-blocks of four 16-byte words per lane, the next one on its way.  It leaves the
+// of it in sub-blocks of four words of 16 bytes per lane, the next one on its way.  It leaves the
 // segment's largest logit, its sum of exponentials and its best K logits in order: within a
 // row totals are ordered as logits, so no other candidate can be kept, whatever the row's sum
 // turns out to be.  The merge, a CTA per request, joins the sums, works out the totals of the
@@ -24,13 +24,21 @@
 // ex2's 2^-22 and the rounding of its argument, which average out, and by (x - M) times 1.3e-8,
 // what fp32 drops of log2 e.
 //
+// Words are a row's own (8 or 4 tokens from its start), and a lane's terms, and the order in which
+// they and the lanes' sums are added, go by the token alone.  So beams with the same logits have the
+// same sum, bit for bit, and totals that are equal keep the order of (i, t).  Where the vocabulary is no
+// multiple of 8 (4) a row starts inside a 16-byte word, and its words are put together from two, a
+// neighbouring lane's among them.
+//
 // The logits are read once, everything else is a few KB per request: 64 x 8 x 131071 bf16 is 134 MB,
-// 20 us at the copy rate, and takes 32.5: the stream alone, without exponentials, about 24, 2.5 from
-// there to the lists, 5 the merge.  All CTAs are resident at once and end together, so what follows
-// the stream is paid in full: with a bound, a list and a ranking of its own for every warp the call
-// took 36.5, parts of 2048 words 37.4, a segment in registers and bisected there 47.5.  Four CTAs per
-// SM; five or six, with fewer registers, were slower (43 to 44).  One request of 4 x 32768 takes 7.0
-// us, two launches of little work, with parts halved until the SMs have a CTA each.
+// 20 us at the copy rate, and takes 35.6, of 131072 tokens 33: putting the words together costs 2.4,
+// issue slots (fp16 3.9, fp32 1.4; with constant shifts, a case for each of the seven starts, 1.2 more).
+// Of the 33 the stream alone, without exponentials, takes about 24, 2.5 from there to the lists, 5 the
+// merge.  All CTAs are resident at once and end together, so what follows the stream is paid in full:
+// with a bound, a list and a ranking of its own for every warp the call took 4 more, with parts of
+// 2048 words 5, with a segment in registers and bisected there 15.  Four CTAs per SM; five or six,
+// with fewer registers, were slower (by 10).  One request of 4 x 32768 takes 7.0 us, two launches of
+// little work, with parts halved until the SMs have a CTA each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -153,6 +161,30 @@ struct Logits<__nv_bfloat16> : Logits16<__nv_bfloat16, __nv_bfloat162> {
   }
 };
 
+// A row's words from 16-byte words, SKIP registers and `shift` bits into which they start.  w: this
+// lane's of a sub-block (word k: 32 k + lane), in which the row's words end; they start in the words
+// before, which lane - 1 has, or for lane 0 lane 31, one k earlier (carry: of the sub-block before; left
+// for the next).
+template <int SKIP>
+__device__ __forceinline__ void align_words(uint4 (&w)[4], uint4& carry, int lane, int shift) {
+  const uint4 last = w[3];
+#pragma unroll
+  for (int k = 3; k >= 0; --k) {
+    const uint4 p = k ? w[k ? k - 1 : 0] : carry;
+    const uint32_t own[4] = {w[k].x, w[k].y, w[k].z, w[k].w}, before[4] = {p.x, p.y, p.z, p.w};
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = i < SKIP ? 0u : __shfl_sync(0xffffffffu, lane == 31 ? before[i] : own[i], (lane + 31) & 31);
+      c[4 + i] = own[i];
+    }
+    w[k] = make_uint4(__funnelshift_r(c[SKIP], c[SKIP + 1], shift), __funnelshift_r(c[SKIP + 1], c[SKIP + 2], shift),
+                      __funnelshift_r(c[SKIP + 2], c[SKIP + 3], shift),
+                      __funnelshift_r(c[SKIP + 3], c[SKIP + 4], shift));
+  }
+  carry = last;
+}
+
 template <class T>
 struct ScanSmem {
   T most[kScanWarps][beam_part_words(sizeof(T)) / 128][32];   // every lane's largest of each sub-block
@@ -172,36 +204,41 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t K = static_cast<uint32_t>(p.beams);
   const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits;
-  // The row's words by their 16-byte boundaries; its first and last may be other rows' as well.
-  // This warp: words a0 .. a1 - 1 of them
+  // The row's words: word g holds tokens g VEC .. g VEC + VEC - 1, wherever the row starts, so that rows
+  // with the same logits are summed and listed alike and totals that are equal stay equal.  In memory
+  // word g starts `lead` logits into 16-byte word g (from src) and, if lead is not 0, ends in the next.
+  // This warp: words a0 .. a1 - 1
   const int64_t r0 = static_cast<int64_t>(row) * p.vocab, w0 = r0 / VEC;
-  const int lead = static_cast<int>(r0 - w0 * VEC);
-  const int words = (lead + p.vocab + VEC - 1) / VEC, cut = words * VEC - lead - p.vocab;
+  const int lead = static_cast<int>(r0 - w0 * VEC), next = lead > 0 ? 1 : 0;
+  const int words = (p.vocab + VEC - 1) / VEC;
   const int a0 = split * p.seg_words + warp * p.part_words;
   const int a1 = min(words, min((split + 1) * p.seg_words, a0 + p.part_words));
   const int subs = a1 > a0 ? (a1 - a0 + 127) / 128 : 0;
   const uint4* src = static_cast<const uint4*>(p.logits) + w0;
-  // the buffer may end inside the last row's last word
-  const int whole = cut > 0 && row + 1 == p.batch * p.beams ? words - 1 : words;
-  // words with odd logits: before and behind the row's own, and the one that ends a sequence,
-  // which is the merge's
-  const int odd0 = lead > 0 ? 0 : -1, odd1 = cut > 0 ? words - 1 : -1;
-  const int odd2 = p.eos >= 0 ? (p.eos + lead) / VEC : -1;
-  auto load = [&](int g) {
-    return g < a1 && g < whole ? src[g] : make_uint4(G::kHidden, G::kHidden, G::kHidden, G::kHidden);
-  };
-  // hides a word's odd logits, and loads the others of an open last word
+  // the buffer may end inside a 16-byte word: `whole` are there in full, and with them the tokens below
+  // `safe`
+  const int whole = static_cast<int>(
+      min(static_cast<int64_t>(words) + 1, static_cast<int64_t>(p.batch) * p.beams * p.vocab / VEC - w0));
+  const int safe = whole * VEC - lead;
+  // words with odd logits: from odd1 on (past the vocabulary, or not in a whole 16-byte word), and the
+  // one that ends a sequence, which is the merge's
+  const int odd1 = min(p.vocab / VEC, max(safe, 0) / VEC);
+  const int odd2 = p.eos >= 0 ? p.eos / VEC : -1;
+  const uint4 hidden = make_uint4(G::kHidden, G::kHidden, G::kHidden, G::kHidden);
+  // the 16-byte word in which word g ends
+  auto load = [&](int g) { return g < a1 && g + next < whole ? src[g + next] : hidden; };
+  // hides a word's odd logits, and loads those of an open 16-byte word
   auto mend = [&](int g, uint4& w) {
-    if (g >= a1 || (g != odd0 && g != odd1 && g != odd2)) return;
+    if (g >= a1 || (g < odd1 && g != odd2)) return;
     uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const int t = g * VEC + e - lead;
+      const int t = g * VEC + e;
       const uint32_t mask = VEC == 4 ? 0xFFFFFFFFu : 0xFFFFu << ((e & 1) * 16);
       uint32_t& x = v[e * 4 / VEC];
-      if (t < 0 || t >= p.vocab || t == p.eos)
+      if (t >= p.vocab || t == p.eos)
         x = (x & ~mask) | (G::kHidden & mask);
-      else if (g >= whole)
+      else if (t >= safe)
         x = (x & ~mask) | G::bits(static_cast<const T*>(p.logits)[r0 + t]) << (VEC == 4 ? 0 : (e & 1) * 16);
     }
     w = make_uint4(v[0], v[1], v[2], v[3]);
@@ -223,10 +260,12 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
   griddep_launch();
   // ---- this lane's largest logit m and its sum s of exp(x - m)
   float m = -INFINITY, s = 0.f;
-  uint4 w[4], ahead[4];
+  uint4 w[4], ahead[4], carry = hidden;   // carry: (lane 31) the 16-byte word before a sub-block's
+  constexpr int kBytes = sizeof(T);
+  const int skip = lead * kBytes / 4, shift = lead * kBytes % 4 * 8;
   auto load_sub = [&](int first) {
-    if (first + 128 <= min(a1, whole)) {
-      const uint4* at = src + first + lane;
+    if (first + 128 <= min(a1, whole - next)) {
+      const uint4* at = src + next + first + lane;
 #pragma unroll
       for (int k = 0; k < 4; ++k) ahead[k] = at[32 * k];
     } else {
@@ -235,13 +274,25 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
     }
   };
   load_sub(a0);
+  if (next && subs > 0 && a0 < whole) carry = src[a0];
 #pragma unroll 1
   for (int sub = 0; sub < subs; ++sub) {
     const uint32_t first = a0 + sub * 128;
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = ahead[k];
     if (sub + 1 < subs) load_sub(first + 128);
-    if (odd0 - first < 128u || odd1 - first < 128u || odd2 - first < 128u) {
+    if (next) {
+      if (skip == 0) align_words<0>(w, carry, lane, shift);
+      else if (skip == 1) align_words<1>(w, carry, lane, shift);
+      else if (skip == 2) align_words<2>(w, carry, lane, shift);
+      else align_words<3>(w, carry, lane, shift);
+      if (first + 128 > static_cast<uint32_t>(a1)) {   // (the next part's)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (first + 32 * k + lane >= static_cast<uint32_t>(a1)) w[k] = hidden;
+      }
+    }
+    if (first + 128 > static_cast<uint32_t>(odd1) || odd2 - first < 128u) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) mend(first + 32 * k + lane, w[k]);
     }
@@ -321,6 +372,15 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
       const int at = note[u >> 2];
       const int g = a0 + (at >> 5) * 128 + (u & 3) * 32 + (at & 31);
       uint4 v = load(g);
+      if (next && g < a1) {
+        uint4 c = g < whole ? src[g] : hidden;
+        for (int n = 0; n < skip; ++n) {
+          c = make_uint4(c.y, c.z, c.w, v.x);
+          v = make_uint4(v.y, v.z, v.w, 0);
+        }
+        v = make_uint4(__funnelshift_r(c.x, c.y, shift), __funnelshift_r(c.y, c.z, shift),
+                       __funnelshift_r(c.z, c.w, shift), __funnelshift_r(c.w, v.x, shift));
+      }
       mend(g, v);
       v = make_uint4(G::clean(v.x), G::clean(v.y), G::clean(v.z), G::clean(v.w));
       typename G::Most mk;
@@ -330,7 +390,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
       G::unpack(v, x);
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
-        if (x[e] >= least && x[e] > -INFINITY) f(x[e], g * VEC + e - lead);
+        if (x[e] >= least && x[e] > -INFINITY) f(x[e], g * VEC + e);
     }
     __syncwarp();
   };
