@@ -452,7 +452,7 @@ rcp_status beam_plan(int32_t batch, int32_t beams, int32_t vocab, int32_t dtype,
   constexpr int kWarps = rcp::kBeamScanThreads / 32;
   auto splits = [&](int64_t part) { return (row_words + part * kWarps - 1) / (part * kWarps); };
   int64_t part = rcp::beam_part_words(dtype == RCP_LOGITS_FP32 ? 4 : 2);
-  while (part > 128 && rows * splits(part) < 304) part /= 2;
+  while (part > 128 && rows * splits(part) < rcp::kBeamMinSegments) part /= 2;
   if (rows * splits(part) > INT32_MAX) return RCP_ERR_UNSUPPORTED;
   out->splits = static_cast<int32_t>(splits(part));
   out->seg_words = static_cast<int32_t>((row_words + out->splits - 1) / out->splits);

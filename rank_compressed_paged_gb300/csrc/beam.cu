@@ -542,6 +542,16 @@ __device__ __forceinline__ TwoFloat log_of(TwoFloat s) {
 constexpr int merge_smem_bytes(int beams, int splits) {
   return beams * splits * (12 * beams + 2);
 }
+// The most of any call: one request whose segments were halved once more while it had fewer than 304
+constexpr int merge_smem_most() {
+  int most = 0;
+  for (int k = 1; k <= kMaxBeams; ++k) {
+    const int bytes = merge_smem_bytes(k, 2 * (kBeamMinSegments - 1) / k);
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+static_assert(merge_smem_most() + 2048 <= 227 * 1024, "dynamic and static shared memory of the merge");
 template <class T>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
   extern __shared__ __align__(16) uint8_t merge_smem[];
@@ -680,9 +690,11 @@ static cudaError_t launch_beam_type(const BeamParams& p, cudaStream_t s) {
                              dim3(kScanThreads), 0, s, true, p);
   if (e != cudaSuccess) return e;
   const int smem = merge_smem_bytes(p.beams, p.splits);
+  // the limit is the function's, whichever thread launches it: always the same one, so that no call
+  // lowers it between another's request and launch
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(beam_merge_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem)) != cudaSuccess)
+                                merge_smem_most())) != cudaSuccess)
     return e;
   return launch_pdl(beam_merge_kernel<T>, dim3(p.batch), dim3(kMergeThreads), smem, s, true, p);
 }

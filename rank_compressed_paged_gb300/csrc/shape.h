@@ -278,6 +278,7 @@ struct ReorderParams {
 constexpr int kBeamScanThreads = 256;
 constexpr int beam_part_words(int logit_bytes) { return logit_bytes == 4 ? 16 * 128 : 32 * 128; }
 constexpr int kMaxBeams = 32, kMaxVocab = 1 << 18;
+constexpr int kBeamMinSegments = 304;   // segments of a call below which they are halved
 struct BeamParams {
   const void* logits;         // [batch][beams][vocab]
   const float* scores;        // [batch][beams]
