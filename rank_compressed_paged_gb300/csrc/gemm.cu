@@ -1076,8 +1076,9 @@ static cudaError_t launch_cluster(K kernel, int grid, int cluster, int smem, cud
 template <class S>
 struct AppendCfg {
   static constexpr int KS_SMALL = (S::H * S::D / 64) < 8 ? (S::H * S::D / 64) : 8;
-  // beside rotated keys, where there are several tiles of 64 tokens: every job then finds its SMs at
-  // once (128 tokens 15.8 -> 10.6 us, 192 16.6 -> 11.0)
+  // of rotated keys, where there are several tiles of 64 tokens: every job then finds its SMs at once
+  // (128 tokens 15.8 -> 10.6 us, 192 16.6 -> 11.0).  Keys that come as they are keep the parts of a plain
+  // append, whatever becomes of the queries beside them: a step stores what its append alone would
   static constexpr int KS_TILES = KS_SMALL < 4 ? KS_SMALL : 4;
   // pipeline stages by token tile: every k-block of a split-K value job (or of a key /
   // query job) in flight at once where shared memory allows
@@ -1172,7 +1173,7 @@ cudaError_t launch_append_gemm(const CUtensorMap& w_v, const CUtensorMap& u_k,
                : go(gemm_kernel<S, kModeAppend, 16, KS, AC::STG16>, clusters, KS, smem);
   }
   if (ap.value_tile == 0 && rows <= 256) {
-    if (rot && ap.T > 64) {
+    if (ap.k_pos != nullptr && ap.T > 64) {
       constexpr int KT = AC::KS_TILES, NKT = (S::H / 2 + KT - 1) / KT;
       return go(gemm_kernel<S, kModeAppend, 64, KT, AC::STG64, true>,
                 (ap.T + 63) / 64 * (NM + NKT) + (ap.nq + 63) / 64 * NKT, KT,
