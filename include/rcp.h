@@ -439,6 +439,13 @@ rcp_status rcp_compact_tokens(rcp_cache* cache, const int32_t* block_table,
                               const uint8_t* keep, int32_t batch, int32_t* new_lens,
                               rcp_stream stream);
 
+/* Workspace bytes of rcp_prefill_step_opt with these options, and of the plain calls with NULL: where
+ * options->diff is NULL, what rcp_prefill_reconstruct_workspace_size tells without the room on 4-bit
+ * pages that only a differential prefill takes. */
+rcp_status rcp_prefill_step_workspace_size(const rcp_cache* cache, int32_t max_query_rows,
+                                           int32_t batch, int32_t max_blocks_per_seq,
+                                           const rcp_step_options* options, size_t* bytes);
+
 /* Reorders cached sequences, as beam search does after each selection: row j of num_new becomes
  * a copy of row parents[j] of the num_rows rows of block_table / seq_lens, and goes on by itself.
  * Full pages are shared.  A partly filled last page stays with the first row (lowest j) of its

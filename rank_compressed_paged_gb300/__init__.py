@@ -660,11 +660,19 @@ class PagedCoeffCache:
         _validate_workspace(self.device, workspace)
         return workspace
 
-    def reconstruct_workspace_bytes(self, rows: int, batch: int, max_blocks_per_seq: int) -> int:
+    def reconstruct_workspace_bytes(self, rows: int, batch: int, max_blocks_per_seq: int,
+                                    diff: bool = True) -> int:
+        """Bytes of workspace of a reconstructing prefill.  diff=False: of calls that are given no
+        DiffHeads, which take less on 4-bit pages."""
         n = ctypes.c_size_t()
-        _lib.check("rcp_prefill_reconstruct_workspace_size",
-                   self._lib.rcp_prefill_reconstruct_workspace_size(
-                       self._h, rows, batch, max_blocks_per_seq, ctypes.byref(n)))
+        if diff:
+            _lib.check("rcp_prefill_reconstruct_workspace_size",
+                       self._lib.rcp_prefill_reconstruct_workspace_size(
+                           self._h, rows, batch, max_blocks_per_seq, ctypes.byref(n)))
+        else:
+            _lib.check("rcp_prefill_step_workspace_size",
+                       self._lib.rcp_prefill_step_workspace_size(
+                           self._h, rows, batch, max_blocks_per_seq, None, ctypes.byref(n)))
         return n.value
 
     def prefill_crossover_rows(self) -> int:
@@ -809,11 +817,12 @@ class PagedCoeffCache:
             raise ValueError(f"unknown prefill variant {variant!r}")
         return variant
 
-    def _prefill_scratch(self, workspace, variant: str, rows: int, B: int, mb: int, stream):
+    def _prefill_scratch(self, workspace, variant: str, rows: int, B: int, mb: int, stream, diff=None):
         # quantized pages are widened into the workspace first (both variants)
         if workspace is not None or (variant == "rank" and self.page_format == "fp16"):
             return self._scratch(workspace, rows, stream)
-        return self.workspace(rows, self.reconstruct_workspace_bytes(rows, B, mb), stream)
+        return self.workspace(rows, self.reconstruct_workspace_bytes(rows, B, mb, diff is not None),
+                              stream)
 
     def _prefill_opt(self, mod, rotary, diff, app, q, cu_chunk_lens, block_table, seq_lens, out,
                      ws, stream, variant: str):
@@ -848,7 +857,7 @@ class PagedCoeffCache:
                                     out)
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B, mod, diff)
-        ws = self._prefill_scratch(workspace, variant, rows, B, mb, stream)
+        ws = self._prefill_scratch(workspace, variant, rows, B, mb, stream, diff)
         if mod is not None or rotary is not None or diff is not None:
             self._prefill_opt(mod, rotary, diff, None, q, cu_chunk_lens, block_table, seq_lens, out,
                               ws, stream, variant)
@@ -876,7 +885,7 @@ class PagedCoeffCache:
                                     out)
         mb = int(block_table.shape[1])
         variant = self._prefill_variant(variant, rows, B, mod, diff)
-        ws = self._prefill_scratch(workspace, variant, rows, B, mb, stream)
+        ws = self._prefill_scratch(workspace, variant, rows, B, mb, stream, diff)
         if mod is not None or rotary is not None or diff is not None:
             self._prefill_opt(mod, rotary, diff, (k, v, slot_mapping), q, cu_chunk_lens, block_table,
                               seq_lens, out, ws, stream, variant)

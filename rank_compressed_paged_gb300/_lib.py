@@ -105,6 +105,9 @@ _SIG = {
                                        ctypes.c_size_t, _P]),
     "rcp_prefill_reconstruct_workspace_size": (ctypes.c_int, [_P, _I32, _I32, _I32,
                                                               ctypes.POINTER(ctypes.c_size_t)]),
+    "rcp_prefill_step_workspace_size": (ctypes.c_int, [_P, _I32, _I32, _I32,
+                                                       ctypes.POINTER(StepOptions),
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
     "rcp_prefill_crossover_rows": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "rcp_set_profile_events": (ctypes.c_int, [_P, _P, _P]),
     "rcp_decode_attn_noalloc": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _P, _P]),

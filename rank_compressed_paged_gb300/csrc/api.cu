@@ -1220,6 +1220,16 @@ rcp_status rcp_prefill_reconstruct_workspace_size(const rcp_cache* c, int32_t ma
   return RCP_OK;
 }
 
+rcp_status rcp_prefill_step_workspace_size(const rcp_cache* c, int32_t max_query_rows, int32_t batch,
+                                           int32_t max_blocks_per_seq,
+                                           const rcp_step_options* options, size_t* bytes) {
+  if (!c || !bytes || max_query_rows < 0 || batch < 0 || max_blocks_per_seq < 0)
+    return RCP_ERR_INVALID_ARG;
+  const bool exact = options && options->diff && c->cfg.page_format == RCP_PAGES_INT4;
+  *bytes = recon_ws_bytes(c, max_query_rows, batch, max_blocks_per_seq, exact);
+  return RCP_OK;
+}
+
 rcp_status rcp_prefill_crossover_rows(const rcp_cache* c, int32_t* rows) {
   if (!c || !rows) return RCP_ERR_INVALID_ARG;
   const int64_t R = c->cfg.rank_v, d = c->cfg.head_dim;
