@@ -226,10 +226,11 @@ def _validate_reorder(device, block_table, seq_lens, parents, tail_blocks, new_t
 
 
 def _validate_beams(logits, scores, eos) -> tuple[int, int, int, int]:
-    """logits: [B][K][V] fp16, bf16 or fp32; scores: [B][K] fp32.  Returns (B, K, V, dtype)."""
+    """logits: [B][K][V] fp16, bf16 or fp32, starting on 16 bytes; scores: [B][K] fp32.  Returns
+    (B, K, V, dtype)."""
     import torch
     code = _logits_code(logits.dtype) if isinstance(logits, torch.Tensor) else None
-    if (code is not None and logits.dim() == 3 and logits.is_contiguous()
+    if (code is not None and logits.dim() == 3 and logits.is_contiguous() and not _ptr(logits) & 15
             and isinstance(scores, torch.Tensor) and scores.dtype is torch.float32
             and scores.is_contiguous() and scores.get_device() == logits.get_device() >= 0):
         B, K, V = logits.shape
@@ -240,6 +241,9 @@ def _validate_beams(logits, scores, eos) -> tuple[int, int, int, int]:
                          f"{getattr(logits, 'dtype', type(logits).__name__)}")
     _need("logits", logits, logits.dtype, (None, None, None))
     B, K, V = logits.shape
+    if _ptr(logits) & 15:
+        raise ValueError("logits must start on a 16-byte boundary (a slice of a larger tensor may not: "
+                         f"clone it), got address {_ptr(logits):#x}")
     _need("scores", scores, torch.float32, (B, K), logits.device)
     if eos is not None and not (hasattr(type(eos), "__index__") and 0 <= operator.index(eos) < V):
         raise ValueError(f"eos must be a token of the vocabulary of {V}, got {eos}")
@@ -320,10 +324,10 @@ def beam_workspace_bytes(batch: int, beams: int, vocab: int, dtype) -> int:
 
 
 def beam_select(logits, scores, eos=None, workspace=None, stream=None):
-    """Beam search's selection.  logits: [B][K][V] fp16, bf16 or fp32, as the model left them;
-    scores: [B][K] fp32, the beams' sums of log-probabilities (-inf: a dead beam, such as all but
-    the first in the first step).  A candidate (i, t) has the total scores[i] +
-    log_softmax(logits[i])[t].  Returns (next_scores [B][K] fp32, tokens [B][K] int32, parents
+    """Beam search's selection.  logits: [B][K][V] fp16, bf16 or fp32, as the model left them, starting
+    on a 16-byte boundary; scores: [B][K] fp32, the beams' sums of log-probabilities (-inf: a dead
+    beam, such as all but the first in the first step).  A candidate (i, t) has the total scores[i]
+    + log_softmax(logits[i])[t].  Returns (next_scores [B][K] fp32, tokens [B][K] int32, parents
     [B][K] int32, ended [B][K] fp32): the best K candidates that do not end in token ``eos``, best
     first, equal totals in the order of (i, t), with parents as rows b * K + i of the batch (for
     reorder_sequences); and for each beam the total of its end, if fewer than K of all candidates
