@@ -487,7 +487,10 @@ rcp_status rcp_reorder_sequences(rcp_cache* cache, const int32_t* block_table, i
  * A beam whose score is not finite has no candidates (-inf: a row past a request's live beams; in
  * the first step all but one), nor has a logit of -inf or NaN; +inf counts as the type's largest
  * value.  Where a request has fewer than `beams` candidates the rest is -inf, -1, -1.
- * Totals are compared with 48 bits and rounded to fp32 at the end.  next_scores may be scores.
+ * Totals are compared with 48 bits and rounded to fp32 at the end.  The logarithm of a row's sum is off
+ * by at most 3.6e-6 (3e-7 on random rows), the same for equal rows: beams with the same logits and
+ * scores keep the order of (i, t), others whose totals are nearer than that may come in either order.
+ * next_scores may be scores.
  * workspace: rcp_beam_workspace_size bytes (256-byte aligned), scratch.  Limits: beams <= 32,
  * vocab <= 2^18 (else RCP_ERR_UNSUPPORTED), eos < vocab, batch * beams * vocab any size. */
 rcp_status rcp_beam_workspace_size(int32_t batch, int32_t beams, int32_t vocab, int32_t dtype,

@@ -293,7 +293,7 @@ struct RotatedPlan {
 };
 
 // When the second launch is done, in us, from what a CTA of h heads takes (6.3 + 1.45 h) and one of
-// the values (20.5, 26 by tiles of 128, 256): SMs take a CTA after the other.
+// the values (20.5, 26 by tiles of 128, 256), all measured on fp16 pages: SMs take a CTA after the other.
 float rotated_end(int64_t value_ctas, int32_t tile, int64_t ctas, int32_t heads, int32_t num_sms) {
   const float tv = tile == 128 ? 20.5f : 26.f, t = 6.3f + 1.45f * heads;
   const int64_t rounds = (value_ctas + num_sms - 1) / num_sms;
@@ -312,7 +312,9 @@ float rotated_end(int64_t value_ctas, int32_t tile, int64_t ctas, int32_t heads,
 // that are done first.  Append in us by tile, parts, heads of a CTA (128, 4, 2), (128, 2, 4), (128, 1, 8),
 // (256, 1, 8): 300 tokens 11.7 - 21.7 24.8; 512 - 15.0 22.0 24.8; 1536 (too many CTAs for a split)
 // 22.8 26.3; 2048 39.4 26.7; by groups of 4, 5, 6, 7, 8: 2560 tokens 37.0 33.3 31.1 29.6 37.8; 4096
-// 45.9 44.9 46.1 54.0 52.2; 5000 66.8 62.9 60.8 59.2 68.1.
+// 45.9 44.9 46.1 54.0 52.2; 5000 66.8 62.9 60.8 59.2 68.1.  The same on quantized pages, whose stores
+// take less (E4M3: 300, 2560, 4096 tokens 11.8 28.4 42.9) or more (4-bit: 16.7 68.9 101, where a plain
+// append takes 70.7 130 185).
 RotatedPlan rotated_plan(int32_t T, int32_t nq, bool turned_keys, const rcp_cache_config& cfg,
                          int32_t num_sms) {
   const int32_t H = cfg.num_heads;

@@ -18,11 +18,13 @@
 // logits, a sorted one), each warp finds the best K of its own part, bisecting the K-th largest where
 // even they are too many.
 //
-// Accuracy: candidates of different beams may lie within an fp32 rounding of each other, so totals
-// are compared as sums of two fp32 values (TwoFloat, 48 bits).  x - M is exact in them; the sum of
-// exponentials comes within about 1e-7 in the worst case, a few 1e-8 in practice: a term is off by
-// ex2's 2^-22 and the rounding of its argument, which average out, and by (x - M) times 1.3e-8,
-// what fp32 drops of log2 e.
+// Accuracy: within a row candidates are in the order of their logits, exactly.  Candidates of different
+// beams may lie within an fp32 rounding of each other, so totals are compared as sums of two fp32
+// values (TwoFloat, 48 bits), in which x - M is exact.  What is left is the sum of exponentials: its
+// logarithm is within 3.6e-6 if every error had the same sign (a term is off by ex2's 2^-22, by the
+// rounding of its argument, 2^-20 of a unit at the most, and by 1.4e-8 of it, what fp32 drops of
+// log2 e; about 32 additions on a term's way round by 2^-24 each), and was within 3e-7 on random
+// rows, 5e-7 on rows of equal logits.  Beams whose totals are nearer than that may come in either order.
 //
 // Words are a row's own (8 or 4 tokens from its start), and a lane's terms, and the order in which
 // they and the lanes' sums are added, go by the token alone.  So beams with the same logits have the
@@ -31,9 +33,10 @@
 // neighbouring lane's among them.
 //
 // The logits are read once, everything else is a few KB per request: 64 x 8 x 131071 bf16 is 134 MB,
-// 20 us at the copy rate, and takes 35.6, of 131072 tokens 33: putting the words together costs 2.4,
-// issue slots (fp16 3.9, fp32 1.4; with constant shifts, a case for each of the seven starts, 1.2 more).
-// Of the 33 the stream alone, without exponentials, takes about 24, 2.5 from there to the lists, 5 the
+// 20 us at the copy rate, and takes 34.5, of 131072 tokens 32: putting the words together costs 2.2 in
+// issue slots (fp16 3.6, fp32 0.6).  With shifts that are constants, in a branch for each of the seven
+// starts, it cost 1.2 more, with a copy of the loop for each 7 to 16: rows that start differently then
+// take turns in an SM's instruction cache.  Of the 32 the stream alone, without exponentials, takes about 24, 2.5 from there to the lists, 5 the
 // merge.  All CTAs are resident at once and end together, so what follows the stream is paid in full:
 // with a bound, a list and a ranking of its own for every warp the call took 4 more, with parts of
 // 2048 words 5, with a segment in registers and bisected there 15.  Four CTAs per SM; five or six,

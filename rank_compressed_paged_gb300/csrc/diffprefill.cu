@@ -33,10 +33,10 @@
 // Bound by the products: 2560 cycles a key tile, of about 3100, with 450 between a value product's end
 // and the next one's beginning (the score product that takes its weights' place is issued between
 // them) and the softmax, 1950, beside them.  16 x (4096 + 256): about 460 of the call's 870 us,
-// 9.5e11 operations with the pairs.  Waiting for keys only behind the value product took 16 us more,
-// handing the halves over by stores to the other's shared memory 10 more.  Sending each value tile
-// to both CTAs at once by multicast changed nothing, handing the maxima over ahead of need took
-// longer (839 -> 865 us at the time).
+// 7.2e11 operations with the pairs (34,304 key tiles of a head, 21 MFLOP each).  Waiting for keys only
+// behind the value product took 16 us more, handing the halves over by stores to the other's shared
+// memory 10 more.  Sending each value tile to both CTAs at once by multicast changed nothing, handing
+// the maxima over ahead of need took longer (839 -> 865 us at the time).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -1128,8 +1128,9 @@ cudaError_t prepare_gemm() {
 }
 
 // The append's projections and, when ap.nq > 0, the rank-space queries (a decode's, or a
-// chunked prefill step's when ap.qhi is set), in one launch (either part may be empty).  q_rows: tensor map over the queries [nq][H*d] with
-// the same box as the token maps (64 x 64 when max(T, nq) <= 256, else 64 x 256).
+// chunked prefill step's when ap.qhi is set), in one launch (either part may be empty), or, with more
+// than 192 rows of which some are rotated, two.  q_rows: tensor map over the queries [nq][H*d]; the
+// boxes of all maps as launch.h has them.
 template <class S>
 cudaError_t launch_append_gemm(const CUtensorMap& w_v, const CUtensorMap& u_k,
                                const CUtensorMap& v_rows, const CUtensorMap& k_rows,

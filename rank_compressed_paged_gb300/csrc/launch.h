@@ -42,8 +42,9 @@ template <class S>
 cudaError_t prepare_gemm();
 // The append (k_rows / v_rows: tensor maps over the new tokens' k and v, [T][H*d]) and,
 // when p.nq > 0, the decode's rank-space queries (q_rows over [nq][H*d]) in one launch;
-// boxes 64 x NT with NT = 16 when max(T, nq) <= 16, 64 when it is <= 256, else 256 (128 for the
-// keys and queries of a call with a position rotation).
+// boxes 64 x NT with NT = 16 when max(T, nq) <= 16, 64 when it is <= 256, else 256.  With a position
+// rotation (p.rot_table): 64 up to 192, else 128 for keys and queries and half of p.value_tile for the
+// values (256 where the value rank is no multiple of 256).
 template <class S>
 cudaError_t launch_append_gemm(const CUtensorMap& w_v, const CUtensorMap& u_k,
                                const CUtensorMap& v_rows, const CUtensorMap& k_rows,
